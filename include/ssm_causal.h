@@ -1,7 +1,7 @@
 /*
  * ssm_causal.h -- C ABI of libssm_causal.so, the B200 (sm_100a) Mamba hot path.
  *
- * Three operations, each one call:
+ * Three operations of the hot path, each one call:
  *
  *   ssm_causal_conv1d_fwd       depthwise causal conv1d (+ optional SiLU) over a
  *                               sequence, reading and writing the conv-state cache.
@@ -15,7 +15,12 @@
  *
  * Beside them: ssm_scan_delta_sum and ssm_scan_carry_fold join a prefill split
  * along the sequence, and ssm_gated_conv1d_fwd is the double-gated short causal
- * conv of an LFM2-style conv block (prefill or one decode step).
+ * conv of an LFM2-style conv block (prefill or one decode step).  The other
+ * token mixers of hybrid models: ssm_linear_attention_fwd and
+ * ssm_linear_attention_update (linear attention with a decay per head, for
+ * prompts and for one token), ssm_paged_attention_decode (attention of one new
+ * token over a paged key-value cache) and ssm_kv_cache_evict (that cache cut to
+ * a budget by accumulated attention weight).
  *
  * Sources.  The operators "causal-conv1d, selective-scan, silu, element-mul"
  * and the Mamba state cache that is read and updated by capturing the conv and
@@ -163,8 +168,19 @@ typedef enum ssm_kernel_id {
     SSM_KERNEL_GATED_CONV = 16,     /* double-gated conv, 16-byte vectors of channels that
                                        are contiguous in memory */
     SSM_KERNEL_GATED_CONV_GENERIC = 17, /* double-gated conv, any strides */
-    SSM_KERNEL_GATED_CONV_ROWS = 18 /* double-gated conv, (B, D, L) rows with contiguous time:
+    SSM_KERNEL_GATED_CONV_ROWS = 18, /* double-gated conv, (B, D, L) rows with contiguous time:
                                        16-byte vectors of steps, history by shuffle */
+    SSM_KERNEL_LINATTN_CHUNK = 19,  /* linear attention over a prompt, chunks of 128 tokens on the
+                                       tensor cores: 16-bit q, k, v, out with contiguous head
+                                       dimensions, 16-byte aligned rows, key size <= 128 */
+    SSM_KERNEL_LINATTN_GENERIC = 20, /* linear attention over a prompt, token by token: any
+                                       strides and types, a warp per 4 rows of the state */
+    SSM_KERNEL_LINATTN_STEP = 21,   /* linear attention of one token, 16-byte vectors of the state */
+    SSM_KERNEL_LINATTN_STEP_GENERIC = 22, /* the same, any strides and sizes */
+    SSM_KERNEL_PAGED_DECODE = 23,   /* paged attention of one token on the tensor cores: 16-bit,
+                                       16-byte aligned rows, head size <= 128 */
+    SSM_KERNEL_PAGED_DECODE_GENERIC = 24, /* the same in float32 arithmetic, any strides and types */
+    SSM_KERNEL_KV_EVICT = 25        /* eviction: selection, then the copy of the kept rows */
 } ssm_kernel_id;
 
 /* ------------------------------------------------------------------------ *
@@ -485,6 +501,210 @@ typedef struct ssm_ssu_args {
 
 ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
 
+/* ------------------------------------------------------------------------ *
+ * Linear attention with a decay per head.  Per batch entry b and head h, with
+ * a state S of P values by N keys (the layout of the Mamba-2 state cache) and
+ * the keys and queries of head h / (H / Hk):
+ *
+ *   S_t   = exp(log_decay[b,h,t]) * S_{t-1} + v_t k_t^T
+ *   out_t = scale * S_t q_t
+ *
+ * ssm_linear_attention_fwd -- a prompt of L tokens.
+ *
+ *   q, k       (B, Hk, L, N)  f32 | f16 | bf16, one dtype; Hk divides H, 1 <= N <= 256
+ *   v, out     (B, H, L, P)   q's dtype
+ *   log_decay  (H) or (B, H, L)  f32: the decay's natural logarithm, <= 0 (-inf: forget
+ *              all that came before); positive values are computed as they
+ *              are, until they overflow
+ *   state      (B, H, P, N)   f32, optional: S_0 (absent: zeros)
+ *   state_out  (B, H, P, N)   f32, optional: the state after the last token.  Absent:
+ *              `state`, if given, is updated in place
+ *   seq_lens   (B)            i32, optional: tokens at or past seq_lens[b] are not there
+ *              (a padded batch): their inputs may hold anything, their rows
+ *              of out are left as they were, the state does not see them.
+ *              Values are limited to 0..L
+ *   scale      factor of the output (for example 1 / sqrt(N))
+ *
+ * Any strides.  16-bit types with unit strides along N and P, N <= 128, N and P
+ * multiples of 8 and 16-byte aligned rows run on SSM_KERNEL_LINATTN_CHUNK (the
+ * rows of a token-major projection seen as (B, H, L, N) count); everything
+ * else on SSM_KERNEL_LINATTN_GENERIC.  L = 0, like a seq_len of 0, copies state
+ * to state_out.  out and state_out may not overlap an input; state_out is
+ * either exactly `state` or does not overlap it.
+ *
+ * The chunk kernel's products are of 16-bit factors, summed in float32: the
+ * masked scores and the state that queries read are rounded to q's dtype
+ * (float16 with a power of two taken out, so that neither can overflow); the
+ * state itself is held in float32 and its update sums products of unrounded
+ * weight (see linattn_chunk.cu).
+ *
+ * The workspace holds the end states of the pieces that few long sequences
+ * are cut into: ssm_linear_attention_workspace_size() returns its size in bytes
+ * (0: not needed).  It is any 256-byte aligned device buffer, its contents on
+ * entry do not matter, and it may be freed or reused once the call's work has
+ * run.  workspace == NULL runs every sequence as one piece.
+ *
+ * ssm_linear_attention_update -- one token per sequence.
+ *
+ *   state      (S, H, P, N)   f32 | f16 | bf16: slots of a state cache
+ *   q, k       (B, Hk, N)     f32 | f16 | bf16, one dtype
+ *   v, out     (B, H, P)      q's dtype
+ *   log_decay  (H) or (B, H)  f32
+ *   state_batch_indices (B)   i32, optional, as in ssm_selective_state_update: row b
+ *              reads and writes slot state_batch_indices[b]; an index outside
+ *              [0, S) skips the row.  Without indices S must equal B
+ *   state_out  (S, H, P, N)   state's dtype, optional: receives the new state of the
+ *              slots that are used (the others are left as they were), and
+ *              `state` is only read (for example to be able to take the token
+ *              back).  Absent: `state` is updated in place
+ *
+ * The output is read from the float32 state before that is rounded to a 16-bit
+ * cache.  Any strides, 1 <= N <= 256; unit stride along N, N a multiple of 16 bytes and
+ * 16-byte aligned rows run on SSM_KERNEL_LINATTN_STEP.  Two rows that name the same
+ * slot race, as in ssm_selective_state_update.
+ * ------------------------------------------------------------------------ */
+typedef struct ssm_linattn_args {
+    uint32_t struct_size; /* = sizeof(ssm_linattn_args) */
+    uint32_t flags;       /* SSM_FLAG_* */
+    ssm_tensor q;
+    ssm_tensor k;
+    ssm_tensor v;
+    ssm_tensor log_decay;
+    ssm_tensor state;
+    ssm_tensor state_out;
+    ssm_tensor seq_lens;
+    float scale;
+    ssm_tensor out;
+    ssm_launch_info* info; /* optional */
+    void* workspace;          /* optional device scratch, see above */
+    uint64_t workspace_bytes; /* its size in bytes */
+} ssm_linattn_args;
+
+ssm_status ssm_linear_attention_fwd(const ssm_linattn_args* args, void* stream);
+ssm_status ssm_linear_attention_workspace_size(const ssm_linattn_args* args, uint64_t* bytes);
+
+typedef struct ssm_linattn_update_args {
+    uint32_t struct_size; /* = sizeof(ssm_linattn_update_args) */
+    uint32_t flags;       /* SSM_FLAG_* */
+    ssm_tensor state;
+    ssm_tensor q;
+    ssm_tensor k;
+    ssm_tensor v;
+    ssm_tensor log_decay;
+    ssm_tensor state_batch_indices;
+    ssm_tensor state_out;
+    float scale;
+    ssm_tensor out;
+    ssm_launch_info* info; /* optional */
+} ssm_linattn_update_args;
+
+ssm_status ssm_linear_attention_update(const ssm_linattn_update_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * ssm_paged_attention_decode -- attention of one new token per sequence over a
+ * paged key-value cache, the step of the grouped-query attention blocks that
+ * the LFM2.5 page (section 2.1) names next to the conv blocks.  Token t of sequence b lies in
+ * row t % page of page block_table[b, t / page]; query head h reads the
+ * key-value head h / (Hq / Hkv):
+ *
+ *   p[b,h,t]  = softmax over t < seq_lens[b] of scale * q[b,h] . k[t]
+ *   out[b,h]  = sum_t p[b,h,t] v[t]
+ *
+ *   q, out       (B, Hq, D)            f32 | f16 | bf16; Hkv divides Hq, 1 <= D <= 256
+ *   k_cache, v_cache (pages, page, Hkv, D)  q's dtype
+ *   block_table  (B, M)                i32
+ *   seq_lens     (B)                   i32, the new token included; limited to 0..M*page
+ *   weights      (B, Hkv, T)           f32, optional, in/out: accumulated attention
+ *                weight, weights[b,hk,t] += sum over the query heads of hk of
+ *                p[b,h,t] for t < seq_lens[b]; T >= M * page
+ *   weights_out  (B, Hkv, T)           f32, optional, with weights: receives the sums, and
+ *                weights is only read.  Entries at or past seq_lens[b] are left as they were
+ *   lse          (B, Hq)               f32, optional: log of the softmax's denominator
+ *                (natural logarithm), to join attention over several caches
+ *
+ * A page index outside [0, pages) holds no tokens: they are masked.  A sequence
+ * with no token (or whose every score is -inf) gives out = 0 and lse = -inf and adds
+ * no weight.  Rows of a page past the sequence's end are never read.
+ *
+ * M * page is at most 2^30.
+ *
+ * The work is the list of (sequence, 64 tokens) blocks of all sequences, cut
+ * into equal parts on the device: lengths are never read on the host.  Partial
+ * results are joined by a second kernel through the workspace.
+ * ssm_paged_attention_workspace_size() returns its size; as above its contents
+ * do not matter.  A call without a workspace, or with a smaller one, is refused
+ * (SSM_ERR_WORKSPACE).
+ *
+ * 16-bit types with unit stride along D, D a multiple of 8 up to 128 and 16-byte
+ * aligned rows run on SSM_KERNEL_PAGED_DECODE, everything else on
+ * SSM_KERNEL_PAGED_DECODE_GENERIC.
+ * ------------------------------------------------------------------------ */
+typedef struct ssm_paged_attention_args {
+    uint32_t struct_size; /* = sizeof(ssm_paged_attention_args) */
+    uint32_t flags;       /* SSM_FLAG_* */
+    ssm_tensor q;
+    ssm_tensor k_cache;
+    ssm_tensor v_cache;
+    ssm_tensor block_table;
+    ssm_tensor seq_lens;
+    ssm_tensor weights;
+    ssm_tensor weights_out;
+    ssm_tensor lse;
+    float scale;
+    ssm_tensor out;
+    ssm_launch_info* info; /* optional */
+    void* workspace;          /* device scratch, required, see above */
+    uint64_t workspace_bytes; /* its size in bytes */
+} ssm_paged_attention_args;
+
+ssm_status ssm_paged_attention_decode(const ssm_paged_attention_args* args, void* stream);
+ssm_status ssm_paged_attention_workspace_size(const ssm_paged_attention_args* args, uint64_t* bytes);
+
+/* ------------------------------------------------------------------------ *
+ * ssm_kv_cache_evict -- cut the sequences of a paged key-value cache to a
+ * budget of `keep` tokens per key-value head, by accumulated attention weight.
+ *
+ *   k_cache, v_cache (pages, page, Hkv, D)  f32 | f16 | bf16, in/out
+ *   weights      (B, Hkv, T)      f32: accumulated weights (T >= M * page)
+ *   block_table  (B, M)           i32: the sequences' pages
+ *   seq_lens     (B)              i32, limited to 0..M*page
+ *   new_block_table (B, M2)       i32: the pages that receive the kept tokens,
+ *                                 M2 * page >= keep
+ *   keep, recent                  0 <= recent <= keep, 1 <= keep
+ *   new_weights  (B, Hkv, keep)   f32: the kept tokens' weights, 0 past their number
+ *   new_seq_lens (B)              i32: their number, min(keep, tokens)
+ *   kept         (B, Hkv, keep)   i32: their former positions, ascending, -1 past their number
+ *
+ * Of each sequence and head the last `recent` positions are kept and, of the
+ * others, those of the largest weight: of equal weights (-0 equals 0) the
+ * lowest position first, a NaN below every number.  The kept rows are copied in order of
+ * position: kept token j goes to row j % page of page new_block_table[b, j / page].
+ * Every head of a sequence keeps the same number.  Tokens in a page outside [0, pages)
+ * are not there and cannot be kept; rows for a new page outside [0, pages) are not
+ * written.  The sources are not changed, so sequences may share them; a page
+ * that receives tokens must be listed once in new_block_table and in no sequence of
+ * block_table that has tokens in it (the copy would race with its readers).
+ * M * page, M2 * page and keep are at most 2^30.  kept, new_weights and new_seq_lens may not overlap another argument.
+ * ------------------------------------------------------------------------ */
+typedef struct ssm_kv_evict_args {
+    uint32_t struct_size; /* = sizeof(ssm_kv_evict_args) */
+    uint32_t flags;       /* SSM_FLAG_* */
+    ssm_tensor k_cache;
+    ssm_tensor v_cache;
+    ssm_tensor weights;
+    ssm_tensor block_table;
+    ssm_tensor seq_lens;
+    ssm_tensor new_block_table;
+    int64_t keep;
+    int64_t recent;
+    ssm_tensor new_weights;
+    ssm_tensor new_seq_lens;
+    ssm_tensor kept;
+    ssm_launch_info* info; /* optional */
+} ssm_kv_evict_args;
+
+ssm_status ssm_kv_cache_evict(const ssm_kv_evict_args* args, void* stream);
+
 /* Device-side error record.  Every kernel wait that can only end when
  * something else happens (a bulk copy landing in shared memory, a hand-over
  * published by another warp) is bounded; when one runs out the kernel records
@@ -538,7 +758,8 @@ int ssm_abi_version(void);
  * ssm_device_error_report as compiled into the library, so that bindings can
  * check their layouts: which = 0 tensor, 1 conv1d args, 2 scan args, 3 ssu
  * args, 4 launch info, 5 error report, 6 delta-sum args, 7 carry-fold args,
- * 8 gated-conv args. */
+ * 8 gated-conv args, 9 linear-attention args, 10 linear-attention update args,
+ * 11 paged-attention args, 12 eviction args. */
 size_t ssm_struct_size(int which);
 
 /* The wait budget, in cycles, that a failure test's request of `cycles`

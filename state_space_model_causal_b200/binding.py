@@ -14,6 +14,10 @@ The entry points keep the C names:
 * :func:`ssm_selective_state_update`
 * :func:`ssm_scan_delta_sum`, :func:`ssm_scan_carry_fold` (sequence pieces)
 * :func:`ssm_gated_conv1d_fwd` (double-gated short causal conv)
+* :func:`ssm_linear_attention_fwd`, :func:`ssm_linear_attention_update`
+  (linear attention with a decay per head: a prompt, one token)
+* :func:`ssm_paged_attention_decode` (attention of one token over a paged cache)
+* :func:`ssm_kv_cache_evict` (that cache cut by accumulated attention weight)
 """
 from __future__ import annotations
 
@@ -41,6 +45,8 @@ KERNELS = {
     5: "ssu_vec", 6: "ssu_generic", 7: "scan_vec", 8: "ssu_row", 9: "ssu_tma", 10: "ssu_row_tma",
     11: "scan_m2", 12: "scan_m2_generic", 13: "scan_bal", 14: "delta_sum", 15: "carry_fold",
     16: "gated_conv", 17: "gated_conv_generic", 18: "gated_conv_rows",
+    19: "linattn_chunk", 20: "linattn_generic", 21: "linattn_step", 22: "linattn_step_generic",
+    23: "paged_decode", 24: "paged_decode_generic", 25: "kv_evict",
 }
 
 
@@ -122,6 +128,37 @@ class GatedConvArgs(ctypes.Structure):
                 ("info", ctypes.POINTER(LaunchInfo))]
 
 
+class LinAttnArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("flags", ctypes.c_uint32),
+                ("q", Tensor), ("k", Tensor), ("v", Tensor), ("log_decay", Tensor), ("state", Tensor),
+                ("state_out", Tensor), ("seq_lens", Tensor), ("scale", ctypes.c_float), ("out", Tensor),
+                ("info", ctypes.POINTER(LaunchInfo)), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_uint64)]
+
+
+class LinAttnUpdateArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("flags", ctypes.c_uint32),
+                ("state", Tensor), ("q", Tensor), ("k", Tensor), ("v", Tensor), ("log_decay", Tensor),
+                ("state_batch_indices", Tensor), ("state_out", Tensor), ("scale", ctypes.c_float),
+                ("out", Tensor), ("info", ctypes.POINTER(LaunchInfo))]
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("flags", ctypes.c_uint32),
+                ("q", Tensor), ("k_cache", Tensor), ("v_cache", Tensor), ("block_table", Tensor),
+                ("seq_lens", Tensor), ("weights", Tensor), ("weights_out", Tensor), ("lse", Tensor),
+                ("scale", ctypes.c_float), ("out", Tensor), ("info", ctypes.POINTER(LaunchInfo)),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class KvEvictArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("flags", ctypes.c_uint32),
+                ("k_cache", Tensor), ("v_cache", Tensor), ("weights", Tensor), ("block_table", Tensor),
+                ("seq_lens", Tensor), ("new_block_table", Tensor), ("keep", ctypes.c_int64),
+                ("recent", ctypes.c_int64), ("new_weights", Tensor), ("new_seq_lens", Tensor),
+                ("kept", Tensor), ("info", ctypes.POINTER(LaunchInfo))]
+
+
 _lock = threading.Lock()
 _lib = None
 _override = None  # a library swapped in by using_library() (failure tests)
@@ -169,7 +206,11 @@ def _open(path):
                        ("ssm_selective_state_update", SsuArgs),
                        ("ssm_scan_delta_sum", DeltaSumArgs),
                        ("ssm_scan_carry_fold", CarryFoldArgs),
-                       ("ssm_gated_conv1d_fwd", GatedConvArgs)):
+                       ("ssm_gated_conv1d_fwd", GatedConvArgs),
+                       ("ssm_linear_attention_fwd", LinAttnArgs),
+                       ("ssm_linear_attention_update", LinAttnUpdateArgs),
+                       ("ssm_paged_attention_decode", PagedAttentionArgs),
+                       ("ssm_kv_cache_evict", KvEvictArgs)):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
         fn.argtypes = [ctypes.POINTER(argt), ctypes.c_void_p]
@@ -178,6 +219,11 @@ def _open(path):
     lib.ssm_selective_scan_workspace_size.restype = ctypes.c_int
     lib.ssm_selective_scan_workspace_size.argtypes = [ctypes.POINTER(ScanArgs),
                                                       ctypes.POINTER(ctypes.c_uint64)]
+    for name, argt in (("ssm_linear_attention_workspace_size", LinAttnArgs),
+                       ("ssm_paged_attention_workspace_size", PagedAttentionArgs)):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [ctypes.POINTER(argt), ctypes.POINTER(ctypes.c_uint64)]
     lib.ssm_status_string.restype = ctypes.c_char_p
     lib.ssm_status_string.argtypes = [ctypes.c_int]
     lib.ssm_abi_version.restype = ctypes.c_int
@@ -190,7 +236,8 @@ def _open(path):
     lib.ssm_struct_size.restype = ctypes.c_size_t
     lib.ssm_struct_size.argtypes = [ctypes.c_int]
     for which, st in enumerate((Tensor, Conv1dArgs, ScanArgs, SsuArgs, LaunchInfo, ErrorReport,
-                                DeltaSumArgs, CarryFoldArgs, GatedConvArgs)):
+                                DeltaSumArgs, CarryFoldArgs, GatedConvArgs, LinAttnArgs,
+                                LinAttnUpdateArgs, PagedAttentionArgs, KvEvictArgs)):
         if lib.ssm_struct_size(which) != ctypes.sizeof(st):
             raise ImportError(f"struct layout mismatch for {st.__name__}")
     return lib
@@ -502,6 +549,137 @@ def ssm_gated_conv1d_fwd(x, b_gate, c_gate, weight, bias=None, conv_state=None, 
     _check(_run(library().ssm_gated_conv1d_fwd, a, (x, b_gate, c_gate, weight, bias, conv_state, out), stream),
            "ssm_gated_conv1d_fwd")
     return out
+
+
+def _call_with_workspace(fn, size_fn, what, args, tensors, stream, workspace, optional):
+    """Call an entry point whose workspace holds nothing between calls: "auto"
+    allocates one for this call on its stream (the caching allocator reuses
+    it; a captured graph gets one of its own), a uint8 CUDA tensor is passed
+    as given, None passes none where the entry point can do without."""
+    import torch
+    dev = device_of(tensors)
+    with _on_device(dev):
+        ws = None
+        if isinstance(workspace, str):
+            if workspace != "auto":
+                raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
+            need = ctypes.c_uint64(0)
+            _check(size_fn(ctypes.byref(args), ctypes.byref(need)), what)
+            if need.value:
+                if stream is None:
+                    ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+                else:
+                    with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(dev, stream), device=dev)):
+                        ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        elif workspace is not None:
+            device_of((*tensors, workspace))
+            ws = workspace
+        elif not optional:
+            raise ValueError(f"{what} needs a workspace")
+        if ws is not None:
+            args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        _check(_run(fn, args, tensors, stream), what)
+
+
+def ssm_linear_attention_fwd(q, k, v, log_decay, scale=1.0, state=None, state_out=None, seq_lens=None,
+                             out=None, stream=None, info: Optional[LaunchInfo] = None, workspace="auto"):
+    """Linear attention with a decay per head over a prompt (see
+    include/ssm_causal.h): S_t = exp(log_decay) S_{t-1} + v_t k_t^T,
+    out_t = scale S_t q_t.  q, k (B, Hk, L, N); v (B, H, L, P); log_decay (H)
+    or (B, H, L) float32; state (B, H, P, N) float32, read as S_0 and updated
+    in place, or only read when state_out is given; seq_lens (B) int32.
+    Without ``out``, the output takes v's order of dimensions.  Returns out."""
+    import torch
+    if out is None:
+        out = torch.empty_like(v)
+    a = LinAttnArgs()
+    a.struct_size = ctypes.sizeof(LinAttnArgs)
+    tensors = (q, k, v, log_decay, state, state_out, seq_lens, out)
+    (a.q, a.k, a.v, a.log_decay, a.state, a.state_out, a.seq_lens, a.out) = map(describe, tensors)
+    a.scale = scale
+    a.info = _info_ptr(info)
+    lib = library()
+    _call_with_workspace(lib.ssm_linear_attention_fwd, lib.ssm_linear_attention_workspace_size,
+                         "ssm_linear_attention_fwd", a, tensors, stream, workspace, optional=True)
+    return out
+
+
+def ssm_linear_attention_update(state, q, k, v, log_decay, scale=1.0, state_batch_indices=None,
+                                state_out=None, out=None, stream=None, info: Optional[LaunchInfo] = None):
+    """One token of linear attention per sequence (see include/ssm_causal.h).
+    state (S, H, P, N); q, k (B, Hk, N); v (B, H, P); log_decay (H) or (B, H)
+    float32; state_batch_indices (B) int32 slots.  The state is updated in
+    place, or written to state_out and only read.  Returns out (B, H, P)."""
+    import torch
+    if out is None:
+        out = torch.empty_like(v)
+    a = LinAttnUpdateArgs()
+    a.struct_size = ctypes.sizeof(LinAttnUpdateArgs)
+    tensors = (state, q, k, v, log_decay, state_batch_indices, state_out, out)
+    (a.state, a.q, a.k, a.v, a.log_decay, a.state_batch_indices, a.state_out, a.out) = map(describe, tensors)
+    a.scale = scale
+    a.info = _info_ptr(info)
+    _check(_run(library().ssm_linear_attention_update, a, tensors, stream), "ssm_linear_attention_update")
+    return out
+
+
+def ssm_paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, weights=None,
+                               weights_out=None, lse=None, out=None, stream=None,
+                               info: Optional[LaunchInfo] = None, workspace="auto"):
+    """Attention of one new token per sequence over a paged cache (see
+    include/ssm_causal.h).  q (B, Hq, D); k_cache, v_cache (pages, page, Hkv, D);
+    block_table (B, M) int32; seq_lens (B) int32; scale: 1 / sqrt(D) unless
+    given; weights (B, Hkv, T) float32, to which the attention weights are
+    added (in place, or into weights_out).  Returns out (B, Hq, D)."""
+    import torch
+    if out is None:
+        out = torch.empty_like(q)
+    a = PagedAttentionArgs()
+    a.struct_size = ctypes.sizeof(PagedAttentionArgs)
+    tensors = (q, k_cache, v_cache, block_table, seq_lens, weights, weights_out, lse, out)
+    (a.q, a.k_cache, a.v_cache, a.block_table, a.seq_lens, a.weights, a.weights_out, a.lse,
+     a.out) = map(describe, tensors)
+    a.scale = q.shape[-1] ** -0.5 if scale is None else scale
+    a.info = _info_ptr(info)
+    lib = library()
+    _call_with_workspace(lib.ssm_paged_attention_decode, lib.ssm_paged_attention_workspace_size,
+                         "ssm_paged_attention_decode", a, tensors, stream, workspace, optional=False)
+    return out
+
+
+def ssm_kv_cache_evict(k_cache, v_cache, weights, block_table, seq_lens, new_block_table, keep, recent=0,
+                       new_weights=None, new_seq_lens=None, kept=None, stream=None,
+                       info: Optional[LaunchInfo] = None):
+    """Cut a paged cache's sequences to `keep` tokens per key-value head: the
+    last `recent` and those of the largest accumulated weight, copied in order
+    to the pages of new_block_table (see include/ssm_causal.h).  Returns
+    (new_seq_lens (B) int32, kept (B, Hkv, keep) int32: former positions,
+    new_weights (B, Hkv, keep) float32)."""
+    import torch
+    B, Hkv = block_table.shape[0], k_cache.shape[2]
+
+    def make(shape, dtype):
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=k_cache.device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(k_cache.device, stream),
+                                                         device=k_cache.device)):
+            return torch.empty(shape, dtype=dtype, device=k_cache.device)
+
+    if new_weights is None:
+        new_weights = make((B, Hkv, keep), torch.float32)
+    if new_seq_lens is None:
+        new_seq_lens = make((B,), torch.int32)
+    if kept is None:
+        kept = make((B, Hkv, keep), torch.int32)
+    a = KvEvictArgs()
+    a.struct_size = ctypes.sizeof(KvEvictArgs)
+    tensors = (k_cache, v_cache, weights, block_table, seq_lens, new_block_table, new_weights, new_seq_lens, kept)
+    (a.k_cache, a.v_cache, a.weights, a.block_table, a.seq_lens, a.new_block_table, a.new_weights,
+     a.new_seq_lens, a.kept) = map(describe, tensors)
+    a.keep, a.recent = keep, recent
+    a.info = _info_ptr(info)
+    _check(_run(library().ssm_kv_cache_evict, a, tensors, stream), "ssm_kv_cache_evict")
+    return new_seq_lens, kept, new_weights
 
 
 def ssm_device_error(stream=None) -> int:

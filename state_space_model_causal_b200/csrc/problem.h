@@ -216,6 +216,87 @@ struct CarryFoldProblem {
     const float* h_end; int64_t h_b, h_h, h_p, h_n;
 };
 
+// Linear attention with a decay per head over a prompt: q, k (Bn, Hk, L, N);
+// v, out (Bn, H, L, P); state (Bn, H, P, N) f32; log decay by (b, h, t) strides
+// (0 along b and t: one value per head).
+struct LinAttnProblem {
+    int64_t Bn, H, Hk, L, N, P;
+    int64_t rep;  // H / Hk
+    int io_dt;
+    const void* q; int64_t q_b, q_h, q_t, q_n;
+    const void* k; int64_t k_b, k_h, k_t, k_n;
+    const void* v; int64_t v_b, v_h, v_t, v_p;
+    const float* g; int64_t g_b, g_h, g_t;
+    const float* s_in; int64_t si_b, si_h, si_p, si_n;  // NULL: zeros
+    float* s_out; int64_t so_b, so_h, so_p, so_n;       // NULL: not written
+    const int32_t* lens; int64_t len_b;                 // NULL: every sequence has L tokens
+    float scale;
+    void* out; int64_t o_b, o_h, o_t, o_p;
+};
+
+// Linear attention of one token: state slots (slots, H, P, N); q, k (Bn, Hk, N);
+// v, out (Bn, H, P).
+struct LinAttnStepProblem {
+    int64_t Bn, H, Hk, N, P, slots;
+    int64_t rep;  // H / Hk
+    int io_dt, st_dt;
+    const void* q; int64_t q_b, q_h, q_n;
+    const void* k; int64_t k_b, k_h, k_n;
+    const void* v; int64_t v_b, v_h, v_p;
+    const float* g; int64_t g_b, g_h;
+    const void* s_in; int64_t si_b, si_h, si_p, si_n;
+    void* s_out; int64_t so_b, so_h, so_p, so_n;
+    const int32_t* slot_idx; int64_t ix_b;  // NULL: row b uses slot b
+    float scale;
+    void* out; int64_t o_b, o_h, o_p;
+};
+
+// Attention of one new token over a paged cache.  The (sequence, 64 tokens)
+// blocks of all sequences are cut into `workers` equal ranges for every
+// (key-value head, block of `hpb` query heads); a worker that has part of a
+// sequence leaves its maximum, sum and weighted values in the workspace.
+struct PagedProblem {
+    int64_t Bn, Hq, Hkv, D, pages, M;
+    int page;             // rows per page
+    int64_t G;            // Hq / Hkv
+    int64_t cap;          // M * page: the longest length, < 2^31
+    int hpb;              // query heads per CTA
+    int hblocks;          // ceil(G / hpb)
+    int64_t workers;
+    int io_dt;
+    const void* q; int64_t q_b, q_h, q_d;
+    const void* k; int64_t k_g, k_t, k_h, k_d;  // strides of page, row, head, element
+    const void* v; int64_t v_g, v_t, v_h, v_d;
+    const int32_t* table; int64_t tb_b, tb_m;
+    const int32_t* lens; int64_t len_b;
+    const float* w; int64_t w_b, w_h, w_t;          // NULL: no accumulated weights
+    float* w_out; int64_t wo_b, wo_h, wo_t;
+    float* lse; int64_t lse_b, lse_h;               // NULL: not wanted
+    float scale_log2;     // scale * log2(e)
+    void* out; int64_t o_b, o_h, o_d;
+    float* ws_o;          // [worker][hkv][hblock][2][hpb][D]
+    float2* ws_ml;        // [worker][hkv][hblock][2][hpb]: maximum (log2), sum
+    float* ws_lse2;       // [b][hq]: log2 of the softmax's denominator (with weights)
+    float* ws_s;          // [b][hq][cap]: scores in log2 (with weights)
+};
+
+// Eviction: the selection writes `kept`, new_w and new_lens, the copy follows it.
+struct EvictProblem {
+    int64_t Bn, Hkv, D, pages, M, M2, cap;
+    int page;
+    int64_t keep, recent;
+    int es;  // bytes per element
+    void* k; int64_t k_g, k_t, k_h, k_d;
+    void* v; int64_t v_g, v_t, v_h, v_d;
+    const float* w; int64_t w_b, w_h, w_t;
+    const int32_t* table; int64_t tb_b, tb_m;
+    const int32_t* lens; int64_t len_b;
+    const int32_t* new_table; int64_t nt_b, nt_m;
+    float* new_w; int64_t nw_b, nw_h, nw_j;
+    int32_t* new_lens; int64_t nl_b;
+    int32_t* kept; int64_t kp_b, kp_h, kp_j;
+};
+
 struct Conv1dPlan {
     int kernel;
     int block;
@@ -253,6 +334,20 @@ cudaError_t launch_gated_conv(const GatedConvProblem& p, int kernel, int grid, i
 int gated_conv_ring_smem_bytes();  // dynamic shared memory of the vector kernel's CTA
 int gated_conv_ctas_per_sm();      // CTAs of the vector kernel resident per SM
 int gated_conv_block();            // threads per CTA of both kernels
+cudaError_t launch_linattn_generic(const LinAttnProblem& p, int grid, cudaStream_t s);
+int linattn_generic_block();
+int linattn_generic_rows();  // rows of the state per CTA
+cudaError_t launch_linattn_step(const LinAttnStepProblem& p, int kernel, int grid, cudaStream_t s);
+int linattn_step_block();
+int linattn_step_rows(int st_dt, int64_t N, bool vec);  // rows of the state per CTA
+cudaError_t launch_paged(const PagedProblem& p, int kernel, cudaStream_t s);
+int paged_block();
+int64_t paged_weight_blocks(int64_t cap);  // CTAs per (sequence, key-value head) of the weights' kernel
+int paged_heads_per_cta(int kernel, int64_t G);
+int paged_ctas_per_sm(int kernel, int64_t G, int64_t D);
+cudaError_t launch_evict(const EvictProblem& p, bool vec, int copy_grid, cudaStream_t s);
+int evict_select_block();
+int evict_copy_block();
 cudaError_t launch_delta_sum(const DeltaSumProblem& p, int grid, int block, cudaStream_t s);
 cudaError_t launch_carry_fold(const CarryFoldProblem& p, int grid, int block, cudaStream_t s);
 int scan_m2_rows_per_cta(int64_t N);
