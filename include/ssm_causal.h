@@ -514,8 +514,7 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  *   q, k       (B, Hk, L, N)  f32 | f16 | bf16, one dtype; Hk divides H, 1 <= N <= 256
  *   v, out     (B, H, L, P)   q's dtype
  *   log_decay  (H) or (B, H, L)  f32: the decay's natural logarithm, <= 0 (-inf: forget
- *              all that came before); positive values are computed as they
- *              are, until they overflow
+ *              all that came before; a positive value counts as 0)
  *   state      (B, H, P, N)   f32, optional: S_0 (absent: zeros)
  *   state_out  (B, H, P, N)   f32, optional: the state after the last token.  Absent:
  *              `state`, if given, is updated in place
@@ -532,17 +531,18 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  * to state_out.  out and state_out may not overlap an input; state_out is
  * either exactly `state` or does not overlap it.
  *
- * The chunk kernel's products are of 16-bit factors, summed in float32: the
- * masked scores and the state that queries read are rounded to q's dtype
- * (float16 with a power of two taken out, so that neither can overflow); the
- * state itself is held in float32 and its update sums products of unrounded
- * weight (see linattn_chunk.cu).
+ * The chunk kernel's products are of 16-bit factors, summed in float32.  The
+ * masked scores are rounded to q's dtype once (float16 with a power of two
+ * taken out of every row, so that they cannot overflow); the state is held in
+ * float32, and what is read from it or added to it is split into two 16-bit
+ * numbers.
  *
  * The workspace holds the end states of the pieces that few long sequences
  * are cut into: ssm_linear_attention_workspace_size() returns its size in bytes
  * (0: not needed).  It is any 256-byte aligned device buffer, its contents on
  * entry do not matter, and it may be freed or reused once the call's work has
- * run.  workspace == NULL runs every sequence as one piece.
+ * run.  workspace == NULL runs every sequence as one piece; one that is given
+ * and too small is refused (SSM_ERR_WORKSPACE).
  *
  * ssm_linear_attention_update -- one token per sequence.
  *
@@ -725,6 +725,10 @@ ssm_status ssm_kv_cache_evict(const ssm_kv_evict_args* args, void* stream);
  *     it is unit * (pieces - 1) + piece, less 1 in the second pass.  That
  *     unit's later outputs and final state are wrong, all other units are
  *     complete.
+ *   ssm_linear_attention_fwd (SSM_KERNEL_LINATTN_CHUNK): the CTA that gave up
+ *     exits, its later outputs and its state not written; first_item is its
+ *     number, (b * H + h) * ceil(P / 64) + value block, times the pieces its
+ *     sequences are cut into, plus its piece.
  *   ssm_selective_scan_fwd, x of rank 4 (SSM_KERNEL_SCAN_M2): the same for a
  *     CTA that waited in vain for its predecessor's state tile; first_item is
  *     the unit (b * H + h) * ceil(P / rows per CTA) + row block.

@@ -17,6 +17,9 @@ namespace {
 using namespace ssm;
 
 constexpr int kMaxN = 256;  // keys per state row, elements per head
+constexpr long long kWaitBudget = 4000000000LL;  // cycles (~2 s) before a bounded wait gives up
+
+uint64_t round256(uint64_t v) { return (v + 255) / 256 * 256; }
 
 bool same_view(const ssm_tensor& a, const ssm_tensor& b) {
     if (a.data != b.data || a.dtype != b.dtype || a.ndim != b.ndim) return false;
@@ -135,6 +138,43 @@ ssm_status linattn_impl(const ssm_linattn_args* a, cudaStream_t stream, uint64_t
     p.out = a->out.data;
     p.o_b = sd(a->out, 0); p.o_h = sd(a->out, 1); p.o_t = sd(a->out, 2); p.o_p = sd(a->out, 3);
 
+    // the chunk kernel: TMA boxes of contiguous, aligned rows (no broadcast)
+    bool chunk = esize(io) == 2 && N <= 128 && L > 0 && L <= INT32_MAX - 256 && B <= INT32_MAX && H <= INT32_MAX;
+    for (const ssm_tensor* t : {&a->q, &a->k, &a->v, &a->out}) {
+        chunk = chunk && rows16(*t);
+        for (int i = 0; i < 3; ++i)
+            chunk = chunk && (t->shape[i] == 1 || (t->stride[i] > 0 && t->stride[i] < ((int64_t)1 << 39)));
+    }
+    if (chunk) {
+        const int64_t units = B * H * ((P + linattn_chunk_values() - 1) / linattn_chunk_values());
+        const int64_t chunks = (L + linattn_chunk_tokens() - 1) / linattn_chunk_tokens();
+        const int dev = current_device(dry);
+        // with less than half a wave of CTAs, each sequence in pieces
+        int64_t pieces = std::min<int64_t>(sm_count(dry, dev) / units, chunks / 2);
+        if (pieces < 2 || (!ws_query && !a->workspace)) pieces = 1;
+        int64_t per_piece = (chunks + pieces - 1) / pieces;
+        pieces = (chunks + per_piece - 1) / per_piece;
+        const uint64_t rec = pieces > 1 ? round256((uint64_t)units * pieces * linattn_chunk_record_bytes()) : 0;
+        const uint64_t need = pieces > 1 ? rec + round256((uint64_t)units * pieces * 8) : 0;
+        if (ws_query) {
+            *ws_query = need;
+            return SSM_OK;
+        }
+        if (pieces > 1) {
+            SSM_TRY(ws_ok(a->workspace, a->workspace_bytes, need));
+            const ssm_tensor ws = ws_tensor(a->workspace, need);
+            for (const ssm_tensor* t : {&a->q, &a->k, &a->v, &a->log_decay, &a->seq_lens, &a->state, &so, &a->out})
+                if (present(*t) && overlap(ws, *t)) return SSM_ERR_ALIAS;
+        }
+        if (units > INT32_MAX / pieces) return SSM_ERR_UNSUPPORTED;
+        fill_info(a->info, SSM_KERNEL_LINATTN_CHUNK, (int)(units * pieces), linattn_chunk_block(), linattn_chunk_smem(),
+                  linattn_chunk_values(), units * pieces);
+        if (dry) return SSM_OK;
+        char* ws = static_cast<char*>(a->workspace);
+        return launch_linattn_chunk(p, units, (int)pieces, per_piece, reinterpret_cast<float*>(ws),
+                                    reinterpret_cast<double*>(ws + rec), kWaitBudget, dev, stream) == cudaSuccess
+                   ? SSM_OK : SSM_ERR_CUDA;
+    }
     const int64_t rows = linattn_generic_rows(), blocks = (P + rows - 1) / rows;
     if (B * H > INT32_MAX / blocks) return SSM_ERR_UNSUPPORTED;
     const int grid = (int)(B * H * blocks);
@@ -219,8 +259,6 @@ ssm_status linattn_update_impl(const ssm_linattn_update_args* a, cudaStream_t st
 
 // -------------------------------------------------------- paged attention --
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // per sequence: positions are 32-bit in the kernels
-
-uint64_t round256(uint64_t v) { return (v + 255) / 256 * 256; }
 
 ssm_status paged_impl(const ssm_paged_attention_args* a, cudaStream_t stream, uint64_t* ws_query) {
     if (!a) return SSM_ERR_NULL;

@@ -25,6 +25,9 @@ namespace {
 constexpr int kBlock = 128;   // 4 warps
 constexpr int kWarpRows = 4;  // rows of S per warp of the generic prompt kernel
 
+// a positive log decay counts as 0 (a NaN stays one)
+__device__ __forceinline__ float decay_log(float g) { return g > 0.0f ? 0.0f : g; }
+
 // sum over the warp of each of K values, K a power of two <= 32: the butterfly
 // halves the number of values a lane carries at each step while it can, so K
 // sums take K + log2(32 / K) - 1 shuffles or so instead of 5 K.  Afterwards
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(kBlock) linattn_generic_kernel(const LinAttnPr
         for (int u = 0; u < U; ++u) {
             const int64_t t = t0 + u;
             const bool on = t < len;
-            gn[u] = on ? g[t * p.g_t] : 0.0f;
+            gn[u] = on ? decay_log(g[t * p.g_t]) : 0.0f;
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
                 const int64_t n = lane + 32 * i;
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(kBlock) linattn_step_kernel(const LinAttnStepP
             kf[c][e] = on ? ld_f(p.k, kb + n * p.k_n, p.io_dt) : 0.0f;
             qf[c][e] = on ? ld_f(p.q, qb + n * p.q_n, p.io_dt) : 0.0f;
         }
-    const float lam = expf(p.g[b * p.g_b + h * p.g_h]);
+    const float lam = expf(decay_log(p.g[b * p.g_b + h * p.g_h]));
     float acc[RU];
 #pragma unroll
     for (int r = 0; r < RU; ++r) {
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(kBlock) linattn_step_generic_kernel(const LinA
     const int64_t row = (blockIdx.x - unit * nblk) * (kBlock / 32) + (threadIdx.x >> 5);
     const int64_t slot = p.slot_idx ? p.slot_idx[b * p.ix_b] : b;
     if (slot < 0 || slot >= p.slots || row >= p.P) return;  // warp-uniform
-    const float lam = expf(p.g[b * p.g_b + h * p.g_h]);
+    const float lam = expf(decay_log(p.g[b * p.g_b + h * p.g_h]));
     const float v = ld_f(p.v, b * p.v_b + h * p.v_h + row * p.v_p, p.io_dt);
     const int64_t si = slot * p.si_b + h * p.si_h + row * p.si_p;
     const int64_t so = slot * p.so_b + h * p.so_h + row * p.so_p;

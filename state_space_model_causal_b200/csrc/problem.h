@@ -337,6 +337,14 @@ int gated_conv_block();            // threads per CTA of both kernels
 cudaError_t launch_linattn_generic(const LinAttnProblem& p, int grid, cudaStream_t s);
 int linattn_generic_block();
 int linattn_generic_rows();  // rows of the state per CTA
+int linattn_chunk_block();
+int linattn_chunk_smem();
+int linattn_chunk_tokens();               // tokens per chunk
+int linattn_chunk_values();               // values per CTA
+uint64_t linattn_chunk_record_bytes();    // one state of a CTA
+// pieces > 1: rec holds units * pieces records, rec_g as many doubles
+cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, int pieces, int64_t per_piece, float* rec,
+                                 double* rec_g, long long wait_budget, int dev, cudaStream_t s);
 cudaError_t launch_linattn_step(const LinAttnStepProblem& p, int kernel, int grid, cudaStream_t s);
 int linattn_step_block();
 int linattn_step_rows(int st_dt, int64_t N, bool vec);  // rows of the state per CTA
