@@ -22,14 +22,17 @@
 //          differences of two sums keep float accuracy however large the sums
 //   3      allocates tensor memory
 //   4-7    scores: tensor memory -> exp(G_t - G_s), mask -> 16 bits -> tensor memory
-//   8-11   V~, and the state: float32 in registers (lane = key, 64 values)
-//   12-15  output
+//          (in place).  With R the sum at the end of s's 32 tokens, exp(G_t - G_s) =
+//          exp(G_t - R) exp(R - G_s), a factor per row and one per column; an exponential
+//          per element only where the 32 tokens of the diagonal decay by more than 2^100
+//   8-11   the state: float32 in registers (lane = key, 64 values)
+//   12-15  V~ of the next chunk, then the output of this one
 //
-// Precision.  Accumulators and S are float32.  V~ and the S that Q S reads are
-// given to the tensor cores as two 16-bit numbers, the second holding what
-// rounding the first left over (16 bits of significand for bf16, 22 for f16): the state is
-// a float32 result and remembers for long.  The scores are rounded once, as the
-// output will be.  For f16, whose range is small, a power of two is taken out of every row of
+// Precision.  Accumulators and S are float32.  V~ is given to the tensor cores as
+// two 16-bit numbers, the second holding what rounding the first left over (16
+// bits of significand for bf16, 22 for f16), because the state is a float32 result and
+// remembers for long.  The scores, and the copy of S that Q S reads, are
+// rounded once, as the output will be.  For f16, whose range is small, a power of two is taken out of every row of
 // scores, of V~ and of S, and put back in float32: it costs three maxima.
 //
 // Few long sequences: with less than one CTA per SM, each is cut into pieces of
@@ -51,27 +54,29 @@ constexpr int DV = 64;        // values per CTA
 constexpr int kBlockBytes = C * 128;               // a tile: 128 rows of 64 16-bit elements
 constexpr int kStageBytes = 5 * kBlockBytes;       // Q (2 tiles), K (2), V (1)
 constexpr int kOffVt = 2 * kStageBytes;            // V~ high, low
-constexpr int kOffS = kOffVt + 2 * kBlockBytes;    // S high, low
-constexpr int kTiles = kOffS + 2 * kBlockBytes;    // 229,376 bytes
+constexpr int kOffS = kOffVt + 2 * kBlockBytes;    // S
+constexpr int kTiles = kOffS + kBlockBytes;        // 212,992 bytes
 
 struct Small {
     uint64_t full_qk[2], full_v[2], empty_qk[2], empty_v[2];  // loads
     uint64_t g_full[2], g_empty[2];                           // decay sums
-    uint64_t sc_full[2], sc_empty[2];                         // scores' accumulators
-    uint64_t p_full, vt_full, kv_full, s_full, qs_done, o_full, o_empty, red_full, spare;
+    uint64_t sc_full[2];                                      // scores' accumulators
+    uint64_t p_full, vt_full, kv_full, kv_empty, s_full, qs_done, o_full, o_empty, red_full[2], spare;
     uint32_t tmem;
     int abort;
-    float red[2][4];
-    int s_lift[2];         // f16: S was divided by 2^s_lift
-    int8_t row_lift[2][C]; // f16: a row of scores was divided by 2^row_lift
-    alignas(16) float g_hi[2][C], g_lo[2][C];  // read as vectors
+    uint8_t red[2][2][4];      // f16: exponents of the largest values, per warp
+    int s_lift[2], v_lift[2];  // f16: S, V~ were divided by 2^lift
+    int8_t row_lift[2][C];     // f16: so was a row of scores
+    alignas(16) float g_hi[2][C], column[2][C];  // read as vectors
+    __half g_lo[2][C];         // remainder of g_hi, below 2^-24 of it
 };
 constexpr int kSmem = kTiles + sizeof(Small);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 static_assert(kTiles % 16 == 0, "alignment of the vectors behind the tiles");
 
 // tensor memory columns
-constexpr uint32_t kSc = 0, kP = 256, kOa = 320, kOb = 384, kKv = 448, kColumns = 512;
+// (the weights P take the first 64 of their scores' 128 columns)
+constexpr uint32_t kSc = 0, kOa = 256, kOb = 320, kKv = 384, kColumns = 512;
 
 struct ChunkArgs {
     LinAttnProblem p;
@@ -80,29 +85,34 @@ struct ChunkArgs {
     int pieces;          // pieces per sequence
     int64_t per_piece;   // chunks per piece
     int states_only;     // first of two launches
+    int out32;           // rows of out are whole, aligned 32-byte sectors
     float* rec;          // [unit][S_0, ends of pieces 0 .. pieces - 2][64 values][128 keys]
     double* rec_g;       // [unit][pieces]: log2 of the piece's decay
     DeviceError* err;
     long long wait_budget;
 };
 
-// Bounded wait; a wait that runs out ends every role of the CTA.
+// Bounded wait; a wait that runs out ends every role of the CTA.  The part that
+// spins is out of line: the warps' code has to stay in the instruction cache
+// (see the note on code size at the kernel).
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* abort, DeviceError* err, long long budget) {
+    const long long t0 = clock64();
+    for (;;) {
+        if (mbar_try(bar, parity)) return true;
+        if (*(volatile int*)abort) return false;
+        if (clock64() - t0 > budget) {
+            *(volatile int*)abort = 1;
+            report_device_error(err, SSM_KERNEL_LINATTN_CHUNK, (long long)blockIdx.x);
+            return false;
+        }
+    }
+}
 struct Waiter {
     Small* sm;
     const ChunkArgs* a;
     // by one thread
     __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
-        if (mbar_try(bar, parity)) return true;
-        const long long t0 = clock64();
-        for (;;) {
-            if (mbar_try(bar, parity)) return true;
-            if (*(volatile int*)&sm->abort) return false;
-            if (clock64() - t0 > a->wait_budget) {
-                *(volatile int*)&sm->abort = 1;
-                report_device_error(a->err, SSM_KERNEL_LINATTN_CHUNK, (long long)blockIdx.x);
-                return false;
-            }
-        }
+        return mbar_try(bar, parity) || wait_long(bar, parity, &sm->abort, a->err, a->wait_budget);
     }
     // by a whole warp, with one answer
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
@@ -132,28 +142,35 @@ template <> struct Half16<__nv_bfloat16> {
     }
 };
 
-// e with top * 2^-e in [2^13, 2^14), where top >= 0 is finite and not 0 (else
-// 0); limited so that 2^e and 2^-e are normal numbers.
-__device__ __forceinline__ int lift_of(float top) {
-    const int e = (int)(__float_as_uint(top) >> 23) - 127 - 13;
-    return top > 0.0f && top < INFINITY ? min(max(e, -120), 120) : 0;
+// e with top * 2^-e in [2^13, 2^14), from the exponent field of top >= 0 (0 if top is 0 or not
+// finite); limited so that 2^e and 2^-e are normal numbers.
+__device__ __forceinline__ int lift_of(uint32_t exponent) {
+    return exponent == 0 || exponent == 255 ? 0 : min(max((int)exponent - 127 - 13, -120), 120);
 }
+__device__ __forceinline__ uint32_t exponent_of(float v) { return __float_as_uint(v) >> 23 & 255u; }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// two 16-bit numbers per value: f = hi + lo, for 8 values
+// two 16-bit numbers per value: f = hi + lo, for a pair
 template <typename T>
-__device__ __forceinline__ void split8(const float* f, uint4& hi, uint4& lo) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = Half16<T>::two(f[2 * i], f[2 * i + 1]);
-        const float2 b = Half16<T>::back(h[i]);
-        l[i] = Half16<T>::two(f[2 * i] - b.x, f[2 * i + 1] - b.y);
-    }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
+__device__ __forceinline__ void split2(u64 f, uint32_t& hi, uint32_t& lo) {
+    float x, y;
+    upk(f, x, y);
+    hi = Half16<T>::two(x, y);
+    const float2 back = Half16<T>::back(hi);
+    upk(fsub2(f, pk(back.x, back.y)), x, y);
+    lo = Half16<T>::two(x, y);
 }
 
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Code size: 16 warps run a dozen different loops, each once per chunk.  Unrolled
+// throughout, they did not fit the instruction caches, and warps waited for
+// instructions more than for anything else (10 of 26 stalled warps per issue; 237 us
+// for 4 x 2048 tokens of 32 heads of 128).  So loops over blocks of 32 columns stay loops.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
 linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -162,7 +179,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     extern __shared__ __align__(1024) unsigned char smem[];
     Small& sm = *reinterpret_cast<Small*>(smem + kTiles);
     const LinAttnProblem& p = a.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int n_pieces = a.states_only ? a.pieces - 1 : a.pieces;
     const int64_t unit = blockIdx.x / n_pieces;
     const int piece = (int)(blockIdx.x - unit * n_pieces);
@@ -188,18 +205,19 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             mbar_init(&sm.empty_qk[i], 1);
             mbar_init(&sm.empty_v[i], 1);
             mbar_init(&sm.g_full[i], 1);
-            mbar_init(&sm.g_empty[i], outputs ? 12 : 4);
+            mbar_init(&sm.g_empty[i], outputs ? 12 : 8);
             mbar_init(&sm.sc_full[i], 1);
-            mbar_init(&sm.sc_empty[i], 4);
         }
         mbar_init(&sm.p_full, 4);
         mbar_init(&sm.vt_full, 4);
         mbar_init(&sm.kv_full, 1);
+        mbar_init(&sm.kv_empty, 4);
         mbar_init(&sm.s_full, 4);
         mbar_init(&sm.qs_done, 1);
         mbar_init(&sm.o_full, 1);
         mbar_init(&sm.o_empty, 4);
-        mbar_init(&sm.red_full, 4);
+        mbar_init(&sm.red_full[0], 4);
+        mbar_init(&sm.red_full[1], 4);
         mbar_init(&sm.spare, 1);
         sm.abort = (smem_u32(smem) & 1023u) != 0;  // the swizzle counts from 1024-byte boundaries
         if (sm.abort) report_device_error(a.err, SSM_KERNEL_LINATTN_CHUNK, (long long)blockIdx.x);
@@ -212,12 +230,27 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = sm.tmem;
+    const uint32_t tm = __shfl_sync(0xffffffffu, sm.tmem, 0);
     const Waiter wait{&sm, &a};
     const bool start = sm.abort == 0;
     auto q_tile = [&](int s) { return smem + s * kStageBytes; };
     auto k_tile = [&](int s) { return smem + s * kStageBytes + 2 * kBlockBytes; };
     auto v_tile = [&](int s) { return smem + s * kStageBytes + 4 * kBlockBytes; };
+
+    // the largest value (>= 0) of a warpgroup; both groups that ask, the state's and the
+        // values', have a place of their own
+    // the largest exponent in a warpgroup (group 0: the state's, 1: the values'), at its call i
+    auto group_max = [&](float v, int group, int i, uint32_t& top) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, exponent_of(v));
+        uint8_t* const red = sm.red[group][i & 1];
+        if (lane == 0) {
+            red[warp & 3] = (uint8_t)m;
+            mbar_arrive(&sm.red_full[group]);
+        }
+        if (!wait(&sm.red_full[group], i & 1)) return false;
+        top = max(max(red[0], red[1]), max(red[2], red[3]));
+        return true;
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------- loads --
@@ -251,75 +284,57 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- products --
-        if (lane == 0 && start && n > 0) {
+        if (start && n > 0) {
             constexpr uint32_t d_qk = mma_desc(HT::kType, false, false, 128, 128);
             constexpr uint32_t d_pv = mma_desc(HT::kType, false, true, 128, DV);
-            constexpr uint32_t d_kv = mma_desc(HT::kType, true, true, 128, DV);
+            constexpr uint32_t d_kv = mma_desc(HT::kType, true, true, 128, 2 * DV);
             const uint32_t base = smem_u32(smem);
             const uint64_t vt = tile_desc(base + kOffVt, kBlockBytes), st = tile_desc(base + kOffS, kBlockBytes);
-            constexpr uint64_t kLow = kBlockBytes >> 4;   // the second number's tile
             auto qd = [&](int s) { return tile_desc(base + s * kStageBytes, kBlockBytes); };
             auto kd = [&](int s) { return tile_desc(base + s * kStageBytes + 2 * kBlockBytes, kBlockBytes); };
             auto vd = [&](int s) { return tile_desc(base + s * kStageBytes + 4 * kBlockBytes, kBlockBytes); };
-            // depth step kk of an operand whose row elements are the depth: 32 bytes, 4 to a tile
-            auto along = [](int kk) { return (uint64_t)((kk >> 2) * (kBlockBytes >> 4) + (kk & 3) * 2); };
-            auto down = [](int kk) { return (uint64_t)kk * (2048 >> 4); };  // whose rows are: 16 rows
-            auto qk = [&](int i) {
-                const int s = i & 1;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tm + kSc + s * 128, qd(s) + along(kk), kd(s) + along(kk), d_qk, kk > 0);
-                mma_commit(&sm.sc_full[s]);
-            };
+            // Order: P V of a chunk, the scores of the next, then its two products with the
+            // state.  The output of the first is read while the second runs, the weights
+            // are made while the last two run, the state is brought up to date during the
+            // first two, and a stage is refilled two steps after it was last read.
+            constexpr int kTile = kBlockBytes >> 4, kRows = 2048 >> 4;  // to the next 64 elements, 16 rows
             bool ok = true;
-            if (outputs) {
-                ok = wait.one(&sm.full_qk[0], 0);
-                if (ok) qk(0);
-            }
-            for (int i = 0; ok && i < n; ++i) {
-                const int s = i & 1;
-                const uint32_t ph = (i >> 1) & 1;
-                ok = wait.one(&sm.vt_full, i & 1) && wait.one(&sm.full_qk[s], ph);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 16; ++kk)
-                    mma_ss(tm + kKv, kd(s) + down(kk & 7), vt + (kk >> 3) * kLow + down(kk & 7), d_kv, kk > 0);
-                mma_commit(&sm.kv_full);
-                if (!outputs) {
-                    mma_commit(&sm.empty_qk[s]);
-                    mma_commit(&sm.empty_v[s]);
-                    continue;
-                }
-                ok = wait.one(&sm.s_full, i & 1) && (i == 0 || wait.one(&sm.o_empty, (i - 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 16; ++kk)
-                    mma_ss(tm + kOb, qd(s) + along(kk & 7), st + (kk >> 3) * kLow + down(kk & 7), d_pv, kk > 0);
-                mma_commit(&sm.qs_done);
-                mma_commit(&sm.empty_qk[s]);
-                // the next chunk's scores before this one's weighted values, if its tiles are here
-                const int j = i + 1, js = j & 1;
-                bool early = false;
-                if (j < n) {
-                    if (j >= 2) ok = wait.one(&sm.sc_empty[js], ((j >> 1) & 1) ^ 1);
+            for (int i = -1; ok && i < n; ++i) {
+                const int s = i & 1, j = i + 1, js = j & 1;
+                const uint32_t ph = (i >> 1) & 1, jph = (j >> 1) & 1;
+                if (outputs) {
+                    if (i >= 0) {
+                        ok = wait(&sm.p_full, i & 1) && wait(&sm.full_v[s], ph);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vs = vd(s);
+                        product_ts<kRows>(tm + kOa, tm + kSc + s * 128, vs, d_pv);
+                        mma_commit(&sm.o_full);
+                        mma_commit(&sm.empty_v[s]);
+                    }
+                    if (j == n) break;
+                    // (the columns held the weights of the chunk before this one's: their
+                    // products were over when that chunk's output was read)
+                    ok = wait(&sm.full_qk[js], jph);
                     if (!ok) break;
-                    early = mbar_try(&sm.full_qk[js], (j >> 1) & 1);
-                    if (early) qk(j);
+                    tc_fence_after();
+                    const uint64_t qs = qd(js), ks = kd(js);
+                    product_ss<2, kTile - 6, 2, kTile - 6>(tm + kSc + js * 128, qs, ks, d_qk);
+                    mma_commit(&sm.sc_full[js]);
                 }
-                ok = wait.one(&sm.p_full, i & 1) && wait.one(&sm.full_v[s], ph);
+                if (j == n) break;
+                // K^T [V~ high | V~ low] (side by side, added up by the state's warps) and Q S
+                ok = wait(&sm.vt_full, j & 1) && wait(&sm.full_qk[js], jph) && (j == 0 || wait(&sm.kv_empty, i & 1)) &&
+                     (!outputs || (wait(&sm.s_full, j & 1) && (j == 0 || wait(&sm.o_empty, i & 1))));
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) mma_ts(tm + kOa, tm + kP + kk * 8, vd(s) + down(kk), d_pv, kk > 0);
-                mma_commit(&sm.o_full);
-                mma_commit(&sm.empty_v[s]);
-                if (j < n && !early) {
-                    ok = wait.one(&sm.full_qk[js], (j >> 1) & 1);
-                    if (ok) qk(j);
-                }
+                const uint64_t ks = kd(js), qs = qd(js);
+                product_ss<kRows, kRows, kRows, kRows>(tm + kKv, ks, vt, d_kv);
+                product_ss<2, kTile - 6, kRows, kRows>(tm + kOb, qs, st, d_pv, outputs);
+                mma_commit(&sm.kv_full);
+                mma_commit(&sm.qs_done);
+                mma_commit(&sm.empty_qk[js]);
+                if (!outputs) mma_commit(&sm.empty_v[js]);
             }
             // every product done before tensor memory is freed
             mma_commit(&sm.spare);
@@ -349,6 +364,8 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                 if (lane >= o) incl += up;
             }
             const double before = incl - x[3];
+            // the sum at the end of this lane's 32 tokens
+            const double end = __shfl_sync(0xffffffffu, incl, lane | 7);
             if (i >= 2) {
                 if (!wait(&sm.g_empty[s], ((i >> 1) & 1) ^ 1)) break;
                 __syncwarp();
@@ -358,7 +375,8 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                 const double G = before + x[j];
                 const float hi = (float)G;
                 sm.g_hi[s][4 * lane + j] = hi;
-                sm.g_lo[s][4 * lane + j] = (float)(G - (double)hi);
+                sm.g_lo[s][4 * lane + j] = __float2half_rn((float)(G - (double)hi));
+                sm.column[s][4 * lane + j] = ex2_approx((float)(end - G));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.g_full[s]);
@@ -370,181 +388,302 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         for (int i = 0; start && outputs && i < n; ++i) {
             const int s = i & 1;
             const uint32_t ph = (i >> 1) & 1;
-            if (!wait(&sm.g_full[s], ph) || !wait(&sm.sc_full[s], ph)) break;
-            if (i > 0 && !wait(&sm.o_full, (i - 1) & 1)) break;  // the last weights are used up
+            if (!wait(&sm.g_full[s], ph)) break;
+            const float hi = sm.g_hi[s][row], lo = __half2float(sm.g_lo[s][row]);
+            if (!wait(&sm.sc_full[s], ph)) break;
             tc_fence_after();
-            const float hi = sm.g_hi[s][row], lo = sm.g_lo[s][row];
+            const uint32_t sc = tm + lanes + kSc + s * 128;
             float lower = 1.0f;
             if (HT::kScaled) {
                 float mx = 0.0f;
+#pragma unroll 1
                 for (int g = 0; g <= w; ++g) {
                     uint32_t r[32];
-                    tmem_ld32(tm + lanes + kSc + s * 128 + g * 32, r);
+                    tmem_ld32(sc + g * 32, r);
+                    const int last = g < w ? 31 : lane;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (g < w || j <= lane) mx = fmaxf(mx, fabsf(__uint_as_float(r[j])));
+                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, j <= last ? fabsf(__uint_as_float(r[j])) : 0.0f);
                 }
-                const int e = lift_of(mx);
+                const int e = lift_of(exponent_of(mx));
                 lower = pow2(-e);
                 sm.row_lift[s][row] = (int8_t)e;
             }
+            // (a product of the two factors on the diagonal is exact enough while the first,
+            // which is above 1 there, and the second stay well inside float32)
+            const bool steep = sm.g_hi[s][w * 32] - sm.g_hi[s][w * 32 + 31] > 100.0f;
+            uint32_t next[32];
+            tmem_ld32_start(sc, next);
 #pragma unroll 1
-            for (int g = 0; g < 4; ++g) {
-                uint32_t out[16];
-                if (g <= w) {
-                    uint32_t r[32];
-                    tmem_ld32(tm + lanes + kSc + s * 128 + g * 32, r);
+            for (int g = 0; g <= w; ++g) {  // (the next block is loaded meanwhile)
+                uint32_t r[32], out[16];
+                tmem_wait_for(next);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 h4 = *reinterpret_cast<const float4*>(&sm.g_hi[s][g * 32 + j]);
-                        const float4 l4 = *reinterpret_cast<const float4*>(&sm.g_lo[s][g * 32 + j]);
-                        const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w};
-                        float e[4];
+                for (int j = 0; j < 32; ++j) r[j] = next[j];
+                if (g < w) tmem_ld32_start(sc + (g + 1) * 32, next);
+                if (g == w && steep) {
+#pragma unroll 1
+                    for (int j = 0; j < 32; ++j) {
+                        // element j of every lane's row, by rotating the registers
+                        const float x = __uint_as_float(r[0]) * lower *
+                                        ex2_approx((hi - sm.g_hi[s][w * 32 + j]) + (lo - __half2float(sm.g_lo[s][w * 32 + j])));
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float d = ex2_approx((hi - hs[u]) + (lo - ls[u]));
-                            float x = __uint_as_float(r[j + u]);
-                            if (HT::kScaled) x *= lower;
-                            e[u] = g < w || j + u <= lane ? x * d : 0.0f;
-                        }
-                        out[j / 2] = HT::two(e[0], e[1]);
-                        out[j / 2 + 1] = HT::two(e[2], e[3]);
+                        for (int u = 0; u < 31; ++u) r[u] = r[u + 1];
+                        r[31] = __float_as_uint(x);
                     }
                 } else {
+                    const int e = g * 32 + 31;
+                    const float f = ex2_approx((hi - sm.g_hi[s][e]) + (lo - __half2float(sm.g_lo[s][e]))) * lower;
+                    const u64 f2 = pk(f, f);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) out[j] = 0u;
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 c4 = *reinterpret_cast<const float4*>(&sm.column[s][g * 32 + j]);
+                        float x0, x1, x2, x3;
+                        upk(fmul2(f2, fmul2(pk(c4.x, c4.y), pk(__uint_as_float(r[j]), __uint_as_float(r[j + 1])))), x0, x1);
+                        upk(fmul2(f2, fmul2(pk(c4.z, c4.w), pk(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])))), x2, x3);
+                        r[j] = __float_as_uint(x0);
+                        r[j + 1] = __float_as_uint(x1);
+                        r[j + 2] = __float_as_uint(x2);
+                        r[j + 3] = __float_as_uint(x3);
+                    }
                 }
-                tmem_st16(tm + lanes + kP + g * 16, out);
+                if (g == w) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = j <= lane ? r[j] : 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) out[j / 2] = HT::two(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                tmem_st16(sc + g * 16, out);
+            }
+#pragma unroll 1
+            for (int g = w + 1; g < 4; ++g) {  // behind it
+                const uint32_t none[16] = {};
+                tmem_st16(sc + g * 16, none);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sm.p_full);
-                mbar_arrive(&sm.sc_empty[s]);
                 mbar_arrive(&sm.g_empty[s]);
             }
         }
     } else if (warp >= 8 && warp < 12) {
-        // ------------------------------------------------------ V~ and state --
-        const int w = warp & 3, row = w * 32 + lane;  // token of V~, key of the state
+        // ------------------------------------------------------------- state --
+        const int w = warp & 3, row = w * 32 + lane;  // this thread's key
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
-        unsigned char* const vt = smem + kOffVt;
         unsigned char* const st = smem + kOffS;
         float S[DV];
         const bool key = row < p.N;
-#pragma unroll
-        for (int j = 0; j < DV; ++j)
-            S[j] = p.s_in && key && p0 + j < p.P && (a.pieces == 1 || (a.states_only && piece == 0))
-                       ? p.s_in[b * p.si_b + h * p.si_h + (p0 + j) * p.si_p + row * p.si_n] : 0.0f;
-        float* const rec = a.rec + unit * a.pieces * (DV * C) + row;  // S_0, then each piece's end
-        if (a.states_only && piece == 0) {
-            // S_0 goes through the workspace: the second launch's last piece may
-            // write state_out, in place, before another piece has begun
+        const int rows = (int)(p.P - p0 < DV ? p.P - p0 : DV);
+        {
+            // (unconditional loads of something valid, so that all are in flight at once)
+            const bool given = p.s_in && key && (a.pieces == 1 || (a.states_only && piece == 0));
+            const float* at = given ? p.s_in + b * p.si_b + h * p.si_h + p0 * p.si_p + row * p.si_n : p.g;
+            const int64_t step = given ? p.si_p : 0;
 #pragma unroll
             for (int j = 0; j < DV; ++j) {
-                rec[j * C] = S[j];
-                S[j] = 0.0f;
+                S[j] = *at;
+                if (j + 1 < rows) at += step;
             }
-        }
-        if (outputs && a.pieces > 1) {  // through the pieces before this one
 #pragma unroll
-            for (int j = 0; j < DV; ++j) S[j] = rec[j * C];
-            for (int i = 0; i < piece; ++i) {
-                const float f = (float)exp2(a.rec_g[unit * a.pieces + i]);
-                const float* end = rec + (i + 1) * (DV * C);
+            for (int j = 0; j < DV; ++j) S[j] = given && j < rows ? S[j] : 0.0f;
+        }
+        float* const rec = a.rec + unit * a.pieces * (DV * C) + row;  // S_0, then each piece's end
+        if (a.states_only) {
+            if (piece == 0) {
+                // S_0 goes through the workspace: the second launch's last piece may
+                // write state_out, in place, before another piece has begun
+#pragma unroll
+                for (int j = 0; j < DV; ++j) rec[j * C] = S[j];
+#pragma unroll
+                for (int j = 0; j < DV; ++j) S[j] = 0.0f;
+            }
+        } else if (a.pieces > 1) {  // through the pieces before this one
+            const float* end = rec;
+            float f = 0.0f;
+#pragma unroll 1
+            for (int i = 0;; ++i) {
 #pragma unroll
                 for (int j = 0; j < DV; ++j) S[j] = fmaf(f, S[j], end[j * C]);
+                if (i == piece) break;
+                f = exp2f((float)a.rec_g[unit * a.pieces + i]);
+                end += DV * C;
             }
         }
-        // the largest of the warpgroup's values (two places, used in turn)
-        uint32_t reds = 0;
-        auto wg_max = [&](float v, float& top) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v));  // v >= 0: ordered as integers
-            float* red = sm.red[reds & 1];
-            if (lane == 0) {
-                red[w] = __uint_as_float(m);
-                mbar_arrive(&sm.red_full);
-            }
-            if (!wait(&sm.red_full, reds & 1)) return false;
-            ++reds;
-            top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-            return true;
-        };
         auto put_state = [&](int i) {  // for the queries of chunk i
             float lower = 1.0f;
             if (HT::kScaled) {
                 float mx = 0.0f;
 #pragma unroll
                 for (int j = 0; j < DV; ++j) mx = fmaxf(mx, fabsf(S[j]));
-                if (!wg_max(mx, mx)) return false;
-                const int e = lift_of(mx);
+                uint32_t top;
+                if (!group_max(mx, 0, i, top)) return false;
+                const int e = lift_of(top);
                 lower = pow2(-e);
                 if (row == 0) sm.s_lift[i & 1] = e;
             }
 #pragma unroll
             for (int j = 0; j < DV; j += 8) {
-                float f[8];
+                uint32_t x[4];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) f[u] = HT::kScaled ? S[j + u] * lower : S[j + u];
-                uint4 hi, lo;
-                split8<T>(f, hi, lo);
-                const int at = row * 128 + (((j >> 3) ^ (row & 7)) << 4);
-                *reinterpret_cast<uint4*>(st + at) = hi;
-                *reinterpret_cast<uint4*>(st + kBlockBytes + at) = lo;
+                for (int u = 0; u < 4; ++u) {
+                    const float f = S[j + 2 * u], g = S[j + 2 * u + 1];
+                    x[u] = HT::kScaled ? HT::two(f * lower, g * lower) : HT::two(f, g);
+                }
+                *reinterpret_cast<uint4*>(st + row * 128 + (((j >> 3) ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.s_full);
             return true;
         };
-        bool ok = start;
-        if (outputs && ok && n > 0) ok = put_state(0);
         double total = 0.0;
-        for (int i = 0; ok && i < n; ++i) {
+        for (int i = 0; start && i < n; ++i) {
+            const int s = i & 1;
+            if (outputs && !((i == 0 || wait(&sm.qs_done, (i - 1) & 1)) && put_state(i))) break;
+            if (!wait(&sm.g_full[s], (i >> 1) & 1)) break;
+            // the decay over the chunk, as its distance from 1 where it is near 1: the
+            // error of a factor near 1 would add up over the chunks S remembers
+            const float end_hi = sm.g_hi[s][C - 1], end_lo = __half2float(sm.g_lo[s][C - 1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.g_empty[s]);
+            const float log2_decay = end_hi + end_lo;
+            total += (double)end_hi + (double)end_lo;
+            const bool near1 = log2_decay > -1.0f;
+            const float f = near1 ? expm1f(log2_decay * kLn2) : ex2_approx(log2_decay);
+            if (!wait(&sm.kv_full, i & 1)) break;
+            tc_fence_after();
+            const float lift = HT::kScaled ? pow2(sm.v_lift[i & 1]) : 1.0f;
+            const u64 lift2 = pk(lift, lift), f2 = pk(f, f);
+#pragma unroll
+            for (int g = 0; g < DV; g += 16) {
+                uint32_t x[16], y[16];
+                tmem_ld16x2(tm + lanes + kKv + g, tm + lanes + kKv + DV + g, x, y);
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    u64 add = fadd2(pk(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                                    pk(__uint_as_float(y[j]), __uint_as_float(y[j + 1])));
+                    if (HT::kScaled) add = fmul2(add, lift2);
+                    const u64 s2 = pk(S[g + j], S[g + j + 1]);
+                    u64 to = ffma2(f2, s2, add);
+                    if (near1) to = fadd2(to, s2);
+                    upk(to, S[g + j], S[g + j + 1]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.kv_empty);
+        }
+        if (start && a.states_only) {
+#pragma unroll
+            for (int j = 0; j < DV; ++j) rec[(piece + 1) * (DV * C) + j * C] = S[j];
+            if (row == 0) a.rec_g[unit * a.pieces + piece] = total;
+        } else if (start && p.s_out && piece == a.pieces - 1 && key) {
+            float* at = p.s_out + b * p.so_b + h * p.so_h + p0 * p.so_p + row * p.so_n;
+#pragma unroll
+            for (int j = 0; j < DV; ++j) {
+                if (j < rows) *at = S[j];
+                at += p.so_p;
+            }
+        }
+    } else if (warp >= 12) {
+        // ---------------------------------------------------- V~ and output --
+        const int w = warp & 3, row = w * 32 + lane;  // this thread's token
+        const uint32_t lanes = (uint32_t)(w * 32) << 16;
+        unsigned char* const vt = smem + kOffVt;
+        T* const out = static_cast<T*>(p.out) + b * p.o_b + h * p.o_h + p0;
+        float across = 0.0f, across_next = 0.0f;  // scale exp(G_t)
+        auto output = [&](int i) {
+            if (!wait(&sm.o_full, i & 1)) return false;
+            tc_fence_after();
+            float inside = p.scale, over = across;
+            if (HT::kScaled) {
+                over *= pow2(sm.s_lift[i & 1]);
+                inside *= pow2(sm.row_lift[i & 1][row]);
+            }
+            const int64_t t = (c0 + i) * C + row;
+            T* const orow = out + t * p.o_t;
+            const u64 over2 = pk(over, over), inside2 = pk(inside, inside);
+#pragma unroll 1
+            for (int g = 0; g < DV; g += 32) {
+                uint32_t x[32], y[32], o[16];
+                tmem_ld32x2(tm + lanes + kOa + g, tm + lanes + kOb + g, x, y);
+                if (g == DV - 32) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.o_empty);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    float f0, f1;
+                    upk(ffma2(pk(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), over2,
+                              fmul2(pk(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), inside2)), f0, f1);
+                    o[j / 2] = HT::two(f0, f1);
+                }
+                if (t < len) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 16) {
+                        if (p0 + g + j >= p.P) break;
+                        if (a.out32) {  // a whole 32-byte sector
+                            store32(orow + g + j, o + j / 2);
+                        } else {
+                            const uint32_t* v = o + j / 2;
+                            *reinterpret_cast<uint4*>(orow + g + j) = make_uint4(v[0], v[1], v[2], v[3]);
+                            if (p0 + g + j + 8 < p.P)
+                                *reinterpret_cast<uint4*>(orow + g + j + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                        }
+                    }
+                }
+            }
+            return true;
+        };
+        auto values = [&](int i) {
             const int s = i & 1;
             const uint32_t ph = (i >> 1) & 1;
-            if (!wait(&sm.g_full[s], ph) || !wait(&sm.full_v[s], ph) || !wait(&sm.full_qk[s], ph)) break;
-            const int64_t t0 = (c0 + i) * C;
-            const bool there = t0 + row < len;
-            unsigned char* vrow = v_tile(s) + row * 128;
-            const float end_hi = sm.g_hi[s][C - 1], end_lo = sm.g_lo[s][C - 1];
-            const float weight = ex2_approx((end_hi - sm.g_hi[s][row]) + (end_lo - sm.g_lo[s][row]));
-            if (!there) {  // rows behind the end may hold anything
+            if (!wait(&sm.g_full[s], ph) || !wait(&sm.full_v[s], ph) || !wait(&sm.full_qk[s], ph)) return false;
+            unsigned char* const vrow = v_tile(s) + row * 128;
+            const float hi = sm.g_hi[s][row], lo = __half2float(sm.g_lo[s][row]);
+            const float weight = ex2_approx((sm.g_hi[s][C - 1] - hi) + (__half2float(sm.g_lo[s][C - 1]) - lo));
+            across_next = ex2_approx(hi) * p.scale;
+            if ((c0 + i) * C + row >= len) {  // rows behind the end may hold anything
                 const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < 8; ++j) {
                     *reinterpret_cast<uint4*>(vrow + 16 * j) = zero;
                     *reinterpret_cast<uint4*>(k_tile(s) + row * 128 + 16 * j) = zero;
                     *reinterpret_cast<uint4*>(k_tile(s) + kBlockBytes + row * 128 + 16 * j) = zero;
                 }
             }
-            float lift = 1.0f, lower = 1.0f;
+            float factor = weight;
+            int lift = 0;
             if (HT::kScaled) {
                 float mx = 0.0f;
-#pragma unroll
+#pragma unroll 2
                 for (int j = 0; j < 8; ++j) {
                     float f[8];
-                    Vec16<T>::unpack(*reinterpret_cast<const uint4*>(vrow + 16 * j), f);
+                    Vec16<T>::unpack(*reinterpret_cast<const uint4*>(vrow + ((j ^ (row & 7)) << 4)), f);
 #pragma unroll
                     for (int u = 0; u < 8; ++u) mx = fmaxf(mx, fabsf(f[u]));
                 }
-                if (!wg_max(mx * weight, mx)) break;
-                const int e = lift_of(mx);
-                lift = pow2(e);
-                lower = pow2(-e);
+                uint32_t top;
+                if (!group_max(mx * weight, 1, i, top)) return false;
+                lift = lift_of(top);
+                factor = weight * pow2(-lift);
             }
-#pragma unroll
+            // the products with the last V~ are over
+            if (i > 0 && !wait(&sm.kv_full, (i - 1) & 1)) return false;
+            if (HT::kScaled && row == 0) sm.v_lift[i & 1] = lift;
+            const u64 factor2 = pk(factor, factor);
+#pragma unroll 2
             for (int j = 0; j < 8; ++j) {
                 const int at = (j ^ (row & 7)) << 4;
                 float f[8];
                 Vec16<T>::unpack(*reinterpret_cast<const uint4*>(vrow + at), f);
+                uint32_t h4[4], l4[4];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) f[u] *= HT::kScaled ? weight * lower : weight;
-                uint4 hi, lo;
-                split8<T>(f, hi, lo);
-                *reinterpret_cast<uint4*>(vt + row * 128 + at) = hi;
-                *reinterpret_cast<uint4*>(vt + kBlockBytes + row * 128 + at) = lo;
+                for (int u = 0; u < 4; ++u) split2<T>(fmul2(factor2, pk(f[2 * u], f[2 * u + 1])), h4[u], l4[u]);
+                *reinterpret_cast<uint4*>(vt + row * 128 + at) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+                *reinterpret_cast<uint4*>(vt + kBlockBytes + row * 128 + at) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -552,82 +691,12 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                 mbar_arrive(&sm.vt_full);
                 mbar_arrive(&sm.g_empty[s]);
             }
-            // the decay over the chunk, as its distance from 1 where it is near 1: the
-            // error of a factor near 1 would add up over the chunks S remembers
-            const float log2_decay = end_hi + end_lo;
-            total += (double)end_hi + (double)end_lo;
-            const bool near1 = log2_decay > -1.0f;
-            const float f = near1 ? expm1f(log2_decay * kLn2) : ex2_approx(log2_decay);
-            if (!wait(&sm.kv_full, i & 1)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t r[32];
-                tmem_ld32(tm + lanes + kKv + g * 32, r);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float x = __uint_as_float(r[j]);
-                    if (HT::kScaled) x *= lift;
-                    float& sj = S[g * 32 + j];
-                    sj = fmaf(f, sj, x) + (near1 ? sj : 0.0f);
-                }
-            }
-            tc_fence_before();
-            if (outputs && i + 1 < n) {
-                if (!wait(&sm.qs_done, i & 1)) break;
-                ok = put_state(i + 1);
-            }
-        }
-        if (start && a.states_only) {
-#pragma unroll
-            for (int j = 0; j < DV; ++j) rec[(piece + 1) * (DV * C) + j * C] = S[j];
-            if (row == 0) a.rec_g[unit * a.pieces + piece] = total;
-        } else if (start && p.s_out && piece == a.pieces - 1 && key) {
-#pragma unroll
-            for (int j = 0; j < DV; ++j)
-                if (p0 + j < p.P) p.s_out[b * p.so_b + h * p.so_h + (p0 + j) * p.so_p + row * p.so_n] = S[j];
-        }
-    } else if (warp >= 12) {
-        // ------------------------------------------------------------ output --
-        const int w = warp & 3, row = w * 32 + lane;
-        const uint32_t lanes = (uint32_t)(w * 32) << 16;
-        T* const out = static_cast<T*>(p.out) + b * p.o_b + h * p.o_h + p0;
-        for (int i = 0; start && outputs && i < n; ++i) {
-            const int s = i & 1;
-            if (!wait(&sm.g_full[s], (i >> 1) & 1)) break;
-            float across = ex2_approx(sm.g_hi[s][row]) * p.scale, inside = p.scale;
-            if (!wait(&sm.o_full, i & 1)) break;
-            tc_fence_after();
-            if (HT::kScaled) {
-                across *= pow2(sm.s_lift[i & 1]);
-                inside *= pow2(sm.row_lift[s][row]);
-            }
-            const int64_t t = (c0 + i) * C + row;
-            T* const orow = out + t * p.o_t;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t x[32], y[32];
-                tmem_ld32(tm + lanes + kOa + g * 32, x);
-                tmem_ld32(tm + lanes + kOb + g * 32, y);
-                if (g == 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sm.o_empty);
-                        mbar_arrive(&sm.g_empty[s]);
-                    }
-                }
-                if (t < len) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        float f[8];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            f[u] = fmaf(__uint_as_float(y[j + u]), across, __uint_as_float(x[j + u]) * inside);
-                        if (p0 + g * 32 + j < p.P) *reinterpret_cast<uint4*>(orow + g * 32 + j) = Vec16<T>::pack(f);
-                    }
-                }
-            }
+            return true;
+        };
+        for (int i = -1; start && i < n; ++i) {
+            across = across_next;
+            if (i + 1 < n && !values(i + 1)) break;
+            if (outputs && i >= 0 && !output(i)) break;
         }
     }
     __syncthreads();
@@ -705,6 +774,8 @@ cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, int pie
     a.per_piece = per_piece;
     a.rec = rec;
     a.rec_g = rec_g;
+    a.out32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.P % 16 == 0 && p.o_b % 16 == 0 && p.o_h % 16 == 0 &&
+              p.o_t % 16 == 0;
     a.err = device_error_ptr(dev);
     if (!a.err) return cudaErrorUnknown;
     a.wait_budget = wait_budget;
