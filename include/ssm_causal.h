@@ -180,7 +180,9 @@ typedef enum ssm_kernel_id {
     SSM_KERNEL_PAGED_DECODE = 23,   /* paged attention of one token on the tensor cores: 16-bit,
                                        16-byte aligned rows, head size <= 128 */
     SSM_KERNEL_PAGED_DECODE_GENERIC = 24, /* the same in float32 arithmetic, any strides and types */
-    SSM_KERNEL_KV_EVICT = 25        /* eviction: selection, then the copy of the kept rows */
+    SSM_KERNEL_KV_EVICT = 25,       /* eviction: selection, then the copy of the kept rows */
+    SSM_KERNEL_LINATTN_STEP_BULK = 26 /* linear attention of one token, the state by bulk copies:
+                                       rows of a multiple of 16 bytes without gaps */
 } ssm_kernel_id;
 
 /* ------------------------------------------------------------------------ *
@@ -560,7 +562,8 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  *
  * The output is read from the float32 state before that is rounded to a 16-bit
  * cache.  Any strides, 1 <= N <= 256; unit stride along N, N a multiple of 16 bytes and
- * 16-byte aligned rows run on SSM_KERNEL_LINATTN_STEP.  Two rows that name the same
+ * 16-byte aligned rows run on SSM_KERNEL_LINATTN_STEP_BULK where a head's rows have no gaps, else on
+ * SSM_KERNEL_LINATTN_STEP.  Two rows that name the same
  * slot race, as in ssm_selective_state_update.
  * ------------------------------------------------------------------------ */
 typedef struct ssm_linattn_args {
@@ -725,6 +728,9 @@ ssm_status ssm_kv_cache_evict(const ssm_kv_evict_args* args, void* stream);
  *     it is unit * (pieces - 1) + piece, less 1 in the second pass.  That
  *     unit's later outputs and final state are wrong, all other units are
  *     complete.
+ *   ssm_linear_attention_update (SSM_KERNEL_LINATTN_STEP_BULK): the CTA that gave up
+ *     exits, what it had not finished neither updated nor written; first_item
+ *     is its number.
  *   ssm_linear_attention_fwd (SSM_KERNEL_LINATTN_CHUNK): the CTA that gave up
  *     exits, its later outputs and its state not written; first_item is its
  *     number, (b * H + h) * ceil(P / 64) + value block, times the pieces its

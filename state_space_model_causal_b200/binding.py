@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -46,7 +47,7 @@ KERNELS = {
     11: "scan_m2", 12: "scan_m2_generic", 13: "scan_bal", 14: "delta_sum", 15: "carry_fold",
     16: "gated_conv", 17: "gated_conv_generic", 18: "gated_conv_rows",
     19: "linattn_chunk", 20: "linattn_generic", 21: "linattn_step", 22: "linattn_step_generic",
-    23: "paged_decode", 24: "paged_decode_generic", 25: "kv_evict",
+    23: "paged_decode", 24: "paged_decode_generic", 25: "kv_evict", 26: "linattn_step_bulk",
 }
 
 
@@ -261,54 +262,80 @@ def raw_tensor(ptr: int, dtype: int, shape: Sequence[int], stride: Optional[Sequ
     return t
 
 
+# ssm_tensor as bytes, by rank (pad bytes are zeros)
+_PACK = {n: struct.Struct(f"=Qii{n}q{8 * (MAX_DIMS - n)}x{n}q{8 * (MAX_DIMS - n)}x") for n in range(1, MAX_DIMS + 1)}
+_DTYPES = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    codes = {torch.float32: SSM_F32, torch.float16: SSM_F16, torch.bfloat16: SSM_BF16,
-             torch.int32: SSM_I32}
-    if t.dtype not in codes:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: SSM_F32, torch.float16: SSM_F16, torch.bfloat16: SSM_BF16,
+                        torch.int32: SSM_I32})
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return codes[t.dtype]
+    return code
+
+
+def _pack_into(buf, offset, t):
+    """torch.Tensor (CUDA) -> ssm_tensor at an offset of a buffer."""
+    if t.get_device() < 0:
+        raise ValueError("libssm_causal takes CUDA tensors only (no CPU fallback)")
+    shape = t.shape
+    pack = _PACK.get(len(shape))
+    if pack is None:
+        raise ValueError(f"rank {t.dim()} is outside 1..{MAX_DIMS}")
+    # an empty tensor's pointer may be NULL, which would mean "absent"
+    pack.pack_into(buf, offset, t.data_ptr() or 16, _dtype_code(t), len(shape), *shape, *t.stride())
 
 
 def describe(t) -> Tensor:
     """torch.Tensor (CUDA) or None -> ssm_tensor."""
-    if t is None:
-        return Tensor()
-    if not t.is_cuda:
-        raise ValueError("libssm_causal takes CUDA tensors only (no CPU fallback)")
-    if t.dim() == 0 or t.dim() > MAX_DIMS:
-        raise ValueError(f"rank {t.dim()} is outside 1..{MAX_DIMS}")
-    return raw_tensor(t.data_ptr() if t.numel() > 0 else max(t.data_ptr(), 16), _dtype_code(t),
-                      tuple(t.shape), tuple(t.stride()))
+    out = Tensor()
+    if t is not None:
+        _pack_into(out, 0, t)
+    return out
+
+
+def _make_args(cls, names, tensors, info=None):
+    """An args struct with its tensor fields filled in (None = absent)."""
+    a = cls()
+    a.struct_size = ctypes.sizeof(cls)
+    for name, t in zip(names, tensors):
+        if t is not None:
+            _pack_into(a, getattr(cls, name).offset, t)
+    if info is not None:
+        a.info = _info_ptr(info)
+    return a
 
 
 def device_of(tensors):
     """The one CUDA device that every given tensor (None = absent) lives on;
     a call whose tensors span devices is refused before anything launches."""
-    devs = {(t.device.type, t.device.index) for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"all tensors of a call must be on one CUDA device, got {sorted(devs)}")
-    return next(t.device for t in tensors if t is not None)
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.device
+        if dev is None:
+            dev = d
+        elif d != dev:
+            dev = None
+            break
+    if dev is None:
+        devs = {(t.device.type, t.device.index) for t in tensors if t is not None}
+        raise ValueError(f"all tensors of a call must be on one CUDA device, got {sorted(devs, key=str)}")
+    return dev
 
 
 def _run(fn, args, tensors, stream):
     """Call a C entry point on the device of its tensors (switching the
     current device only when it differs) and on `stream`, else on that
     device's current stream."""
-    import torch
     dev = device_of(tensors)
-
-    def go():
-        if stream is not None:
-            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        else:
-            handle = torch.cuda.current_stream(dev).cuda_stream
-        return fn(ctypes.byref(args), handle)
-
-    if dev.index is not None and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return go()
-    return go()
+    with _on_device(dev):
+        return fn(ctypes.byref(args), _stream_handle(dev, stream))
 
 
 def _check(status: int, what: str):
@@ -592,12 +619,9 @@ def ssm_linear_attention_fwd(q, k, v, log_decay, scale=1.0, state=None, state_ou
     import torch
     if out is None:
         out = torch.empty_like(v)
-    a = LinAttnArgs()
-    a.struct_size = ctypes.sizeof(LinAttnArgs)
     tensors = (q, k, v, log_decay, state, state_out, seq_lens, out)
-    (a.q, a.k, a.v, a.log_decay, a.state, a.state_out, a.seq_lens, a.out) = map(describe, tensors)
+    a = _make_args(LinAttnArgs, ("q", "k", "v", "log_decay", "state", "state_out", "seq_lens", "out"), tensors, info)
     a.scale = scale
-    a.info = _info_ptr(info)
     lib = library()
     _call_with_workspace(lib.ssm_linear_attention_fwd, lib.ssm_linear_attention_workspace_size,
                          "ssm_linear_attention_fwd", a, tensors, stream, workspace, optional=True)
@@ -613,12 +637,10 @@ def ssm_linear_attention_update(state, q, k, v, log_decay, scale=1.0, state_batc
     import torch
     if out is None:
         out = torch.empty_like(v)
-    a = LinAttnUpdateArgs()
-    a.struct_size = ctypes.sizeof(LinAttnUpdateArgs)
     tensors = (state, q, k, v, log_decay, state_batch_indices, state_out, out)
-    (a.state, a.q, a.k, a.v, a.log_decay, a.state_batch_indices, a.state_out, a.out) = map(describe, tensors)
+    a = _make_args(LinAttnUpdateArgs, ("state", "q", "k", "v", "log_decay", "state_batch_indices", "state_out", "out"),
+                   tensors, info)
     a.scale = scale
-    a.info = _info_ptr(info)
     _check(_run(library().ssm_linear_attention_update, a, tensors, stream), "ssm_linear_attention_update")
     return out
 
@@ -634,13 +656,10 @@ def ssm_paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, scale
     import torch
     if out is None:
         out = torch.empty_like(q)
-    a = PagedAttentionArgs()
-    a.struct_size = ctypes.sizeof(PagedAttentionArgs)
     tensors = (q, k_cache, v_cache, block_table, seq_lens, weights, weights_out, lse, out)
-    (a.q, a.k_cache, a.v_cache, a.block_table, a.seq_lens, a.weights, a.weights_out, a.lse,
-     a.out) = map(describe, tensors)
+    a = _make_args(PagedAttentionArgs, ("q", "k_cache", "v_cache", "block_table", "seq_lens", "weights", "weights_out",
+                                        "lse", "out"), tensors, info)
     a.scale = q.shape[-1] ** -0.5 if scale is None else scale
-    a.info = _info_ptr(info)
     lib = library()
     _call_with_workspace(lib.ssm_paged_attention_decode, lib.ssm_paged_attention_workspace_size,
                          "ssm_paged_attention_decode", a, tensors, stream, workspace, optional=False)
@@ -671,13 +690,10 @@ def ssm_kv_cache_evict(k_cache, v_cache, weights, block_table, seq_lens, new_blo
         new_seq_lens = make((B,), torch.int32)
     if kept is None:
         kept = make((B, Hkv, keep), torch.int32)
-    a = KvEvictArgs()
-    a.struct_size = ctypes.sizeof(KvEvictArgs)
     tensors = (k_cache, v_cache, weights, block_table, seq_lens, new_block_table, new_weights, new_seq_lens, kept)
-    (a.k_cache, a.v_cache, a.weights, a.block_table, a.seq_lens, a.new_block_table, a.new_weights,
-     a.new_seq_lens, a.kept) = map(describe, tensors)
+    a = _make_args(KvEvictArgs, ("k_cache", "v_cache", "weights", "block_table", "seq_lens", "new_block_table",
+                                 "new_weights", "new_seq_lens", "kept"), tensors, info)
     a.keep, a.recent = keep, recent
-    a.info = _info_ptr(info)
     _check(_run(library().ssm_kv_cache_evict, a, tensors, stream), "ssm_kv_cache_evict")
     return new_seq_lens, kept, new_weights
 

@@ -229,12 +229,17 @@ ssm_status linattn_update_impl(const ssm_linattn_update_args* a, cudaStream_t st
         return SSM_OK;
     }
     const bool vec = rows16(a->state) && rows16(so);
-    const int64_t rows = linattn_step_rows(st, N, vec), blocks = (P + rows - 1) / rows;
+    // rows without gaps: bulk copies
+    const bool bulk = vec && (P == 1 || (a->state.stride[2] == N && so.stride[2] == N));
+    const int64_t rows = bulk ? linattn_step_bulk_rows(st, N) : linattn_step_rows(st, N, vec);
+    const int64_t blocks = (P + rows - 1) / rows;
     if (B * H > INT32_MAX / blocks) return SSM_ERR_UNSUPPORTED;
-    const int grid = (int)(B * H * blocks);
-    const int kernel = vec ? SSM_KERNEL_LINATTN_STEP : SSM_KERNEL_LINATTN_STEP_GENERIC;
-    fill_info(a->info, kernel, grid, linattn_step_block(), 0, rows, grid);
-    if (a->flags & SSM_FLAG_DRY_RUN) return SSM_OK;
+    const int items = (int)(B * H * blocks);
+    const int kernel = bulk ? SSM_KERNEL_LINATTN_STEP_BULK : vec ? SSM_KERNEL_LINATTN_STEP : SSM_KERNEL_LINATTN_STEP_GENERIC;
+    const bool dry = (a->flags & SSM_FLAG_DRY_RUN) != 0;
+    const int dev = current_device(dry), sms = sm_count(dry, dev);
+    fill_info(a->info, kernel, bulk ? std::min(items, 2 * sms) : items, linattn_step_block(), 0, rows, items);
+    if (dry) return SSM_OK;
 
     LinAttnStepProblem p{};
     p.Bn = B; p.H = H; p.Hk = Hk; p.N = N; p.P = P; p.slots = S; p.rep = H / Hk; p.io_dt = io; p.st_dt = st;
@@ -254,7 +259,9 @@ ssm_status linattn_update_impl(const ssm_linattn_update_args* a, cudaStream_t st
     }
     p.scale = a->scale;
     p.out = a->out.data; p.o_b = sd(a->out, 0); p.o_h = sd(a->out, 1); p.o_p = sd(a->out, 2);
-    return launch_linattn_step(p, kernel, grid, stream) == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+    const cudaError_t e = bulk ? launch_linattn_step_bulk(p, sms, dev, kWaitBudget, stream)
+                               : launch_linattn_step(p, kernel, items, stream);
+    return e == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
 // -------------------------------------------------------- paged attention --
@@ -433,9 +440,7 @@ ssm_status evict_impl(const ssm_kv_evict_args* a, cudaStream_t stream) {
     p.Bn = B; p.Hkv = Hkv; p.D = D; p.page = (int)page; p.pages = pages; p.M = M; p.M2 = M2; p.cap = cap;
     p.keep = a->keep; p.recent = a->recent; p.es = esize(a->k_cache.dtype);
     const bool vec = D > 0 && rows16(a->k_cache) && rows16(a->v_cache);
-    const int64_t items = B * a->keep * Hkv * (vec ? D * p.es / 16 : D);
-    const int64_t copy_grid = std::max<int64_t>(
-        1, std::min<int64_t>((items + evict_copy_block() - 1) / evict_copy_block(), (int64_t)sm_count(dry) * 64));
+    if (B > INT32_MAX / evict_copy_ctas(a->keep) || Hkv > (1 << 25) || D > (1 << 20)) return SSM_ERR_UNSUPPORTED;
     fill_info(a->info, SSM_KERNEL_KV_EVICT, (int)(B * Hkv), evict_select_block(), 0, 1, B * Hkv);
     if (dry) return SSM_OK;
 
@@ -455,7 +460,7 @@ ssm_status evict_impl(const ssm_kv_evict_args* a, cudaStream_t stream) {
     p.new_lens = static_cast<int32_t*>(a->new_seq_lens.data); p.nl_b = sd(a->new_seq_lens, 0);
     p.kept = static_cast<int32_t*>(a->kept.data);
     p.kp_b = sd(a->kept, 0); p.kp_h = sd(a->kept, 1); p.kp_j = sd(a->kept, 2);
-    return launch_evict(p, vec, (int)copy_grid, stream) == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+    return launch_evict(p, vec, stream) == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
 }  // namespace

@@ -23,6 +23,7 @@ namespace {
 constexpr int kSelect = 512;  // threads of the selection
 constexpr int kSelWarps = kSelect / 32;
 constexpr int kItems = 4;     // consecutive tokens per thread and step
+constexpr int kCached = 48 * 1024;  // keys that fit in shared memory (192 KB)
 constexpr int kCopy = 256;
 
 // Order of the weights as an unsigned key: 0 = a token that cannot be kept,
@@ -35,10 +36,15 @@ __device__ __forceinline__ uint32_t key_of(float w, bool valid, bool recent) {
     return (u >> 31) ? ~u : u | 0x80000000u;       // -inf -> 0x007fffff, +inf -> 0xff800000
 }
 
+// CACHED: the keys are made once and kept in shared memory; else (sequences past
+// 48 Ki tokens) every pass makes them again.
+template <bool CACHED>
 __global__ void __launch_bounds__(kSelect) evict_select_kernel(const EvictProblem p) {
+    extern __shared__ uint32_t keys[];
     __shared__ uint32_t hist[256];
     __shared__ uint32_t sh[kSelWarps];
     __shared__ uint32_t pick[2];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
     int64_t n = p.lens[b * p.len_b];
@@ -47,11 +53,18 @@ __global__ void __launch_bounds__(kSelect) evict_select_kernel(const EvictProble
     const int first_recent = len - (int)(p.recent < n ? p.recent : n);
     const float* w = p.w + b * p.w_b + h * p.w_h;
     const int32_t* table = p.table + b * p.tb_b;
-    auto key_at = [&](int t) {
+    auto make_key = [&](int t) {
         if (t >= len) return 0u;
         const int32_t pg = table[(int64_t)(t / p.page) * p.tb_m];
         return key_of(w[t * p.w_t], pg >= 0 && pg < p.pages, t >= first_recent);
     };
+
+    if (CACHED) {
+#pragma unroll 8
+        for (int t = threadIdx.x; t < len; t += kSelect) keys[t] = make_key(t);
+        __syncthreads();
+    }
+    auto key_at = [&](int t) { return CACHED ? (t < len ? keys[t] : 0u) : make_key(t); };
 
     // passes of 8 bits from the top; `left` tokens are still to be found among
     // the keys that agree with `prefix` in the bits above
@@ -61,14 +74,20 @@ __global__ void __launch_bounds__(kSelect) evict_select_kernel(const EvictProble
         __syncthreads();
         const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
         uint32_t mine = 0;
-        for (int t0 = 0; t0 < len; t0 += kSelect) {
-            const uint32_t key = key_at(t0 + threadIdx.x);
-            mine += key != 0u;
-            const bool on = key != 0u && (key & above) == prefix;
-            // one atomic per distinct digit of the warp: softmax weights share their exponents
-            const uint32_t digit = on ? (key >> shift) & 255u : 256u;
-            const uint32_t same = __match_any_sync(0xffffffffu, digit);
-            if (on && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+        for (int t0 = 0; t0 < len; t0 += 4 * kSelect) {
+            uint32_t key[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) key[u] = key_at(t0 + u * kSelect + threadIdx.x);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                mine += key[u] != 0u;
+                const bool on = key[u] != 0u && (key[u] & above) == prefix;
+                if (!__any_sync(0xffffffffu, on)) continue;
+                // one atomic per distinct digit of the warp: softmax weights share their exponents
+                const uint32_t digit = on ? (key[u] >> shift) & 255u : 256u;
+                const uint32_t same = __match_any_sync(0xffffffffu, digit);
+                if (on && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+            }
         }
         if (shift == 24) {  // how many tokens there are, and how many stay
 #pragma unroll
@@ -124,7 +143,7 @@ __global__ void __launch_bounds__(kSelect) evict_select_kernel(const EvictProble
         for (int i = 0; i < kItems; ++i) {
             const int t = t0 + threadIdx.x * kItems + i;
             const uint32_t key = key_at(t);
-            wv[i] = t < len ? w[t * p.w_t] : 0.0f;
+            wv[i] = key >= prefix ? w[t * p.w_t] : 0.0f;  // (prefix > 0: the token is there)
             gt[i] = key > prefix;
             eq[i] = key == prefix;
             ngt += gt[i];
@@ -167,56 +186,107 @@ __global__ void __launch_bounds__(kSelect) evict_select_kernel(const EvictProble
     if (h == 0 && threadIdx.x == 0) p.new_lens[b * p.nl_b] = (int32_t)stay;
 }
 
-// VEC: rows of 16-byte vectors (unit element stride, aligned); a thread takes a
-// vector of the key row and of the value row.  Else one element.
-template <bool VEC>
+// A CTA takes kRows kept tokens of one sequence for every head: first the offsets of
+// their rows, one thread each (the table look-ups and their arithmetic once per
+// row), then the copy, consecutive threads on consecutive pieces of a row.  VEC: pieces
+// of 16 bytes (unit element stride, aligned rows), else single elements.
+constexpr int kRows = 32;
+
+template <typename W, bool VEC>
 __global__ void __launch_bounds__(kCopy) evict_copy_kernel(const EvictProblem p) {
-    const int64_t per_row = VEC ? p.D * p.es / 16 : p.D;
-    const int64_t total = p.Bn * p.keep * p.Hkv * per_row;
-    const int64_t unit = VEC ? 16 / p.es : 1;  // elements per item
-    for (int64_t i = (int64_t)blockIdx.x * kCopy + threadIdx.x; i < total; i += (int64_t)gridDim.x * kCopy) {
-        int64_t r = i / per_row;
-        const int64_t d = (i - r * per_row) * unit;
-        const int64_t h = r % p.Hkv;
-        r /= p.Hkv;
-        const int64_t j = r % p.keep, b = r / p.keep;
-        const int32_t t = p.kept[b * p.kp_b + h * p.kp_h + j * p.kp_j];
-        const int32_t to = p.new_table[b * p.nt_b + j / p.page * p.nt_m];
-        if (t < 0 || to < 0 || to >= p.pages) continue;
-        const int64_t from = p.table[b * p.tb_b + (int64_t)(t / p.page) * p.tb_m];
-        const int64_t fr = t % p.page, tr = j % p.page;
-        char* k = static_cast<char*>(p.k);
-        char* v = static_cast<char*>(p.v);
-        const int64_t ks = (from * p.k_g + fr * p.k_t + h * p.k_h + d * p.k_d) * p.es;
-        const int64_t kd = (to * p.k_g + tr * p.k_t + h * p.k_h + d * p.k_d) * p.es;
-        const int64_t vs = (from * p.v_g + fr * p.v_t + h * p.v_h + d * p.v_d) * p.es;
-        const int64_t vd = (to * p.v_g + tr * p.v_t + h * p.v_h + d * p.v_d) * p.es;
-        if (VEC) {
-            const uint4 kv = ld_stream16(k + ks), vv = ld_stream16(v + vs);
-            st_stream16(k + kd, kv);
-            st_stream16(v + vd, vv);
-        } else if (p.es == 2) {
-            *reinterpret_cast<uint16_t*>(k + kd) = *reinterpret_cast<const uint16_t*>(k + ks);
-            *reinterpret_cast<uint16_t*>(v + vd) = *reinterpret_cast<const uint16_t*>(v + vs);
-        } else {
-            *reinterpret_cast<uint32_t*>(k + kd) = *reinterpret_cast<const uint32_t*>(k + ks);
-            *reinterpret_cast<uint32_t*>(v + vd) = *reinterpret_cast<const uint32_t*>(v + vs);
+    __shared__ int64_t k_from[kCopy], k_to[kCopy], v_from[kCopy], v_to[kCopy];  // element offsets, k_from < 0: no row
+    const int64_t blocks = (p.keep + kRows - 1) / kRows;
+    const int64_t b = blockIdx.x / blocks, j0 = (blockIdx.x - b * blocks) * kRows;
+    const int rows = (int)(p.keep - j0 < kRows ? p.keep - j0 : kRows);
+    const int entries = rows * (int)p.Hkv;  // (Hkv < 2^26)
+    const int pieces = VEC ? (int)(p.D * p.es / 16) : (int)p.D;
+    const int per = VEC ? 16 / p.es : 1;  // elements per piece
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the selection
+    for (int e0 = 0; e0 < entries; e0 += kCopy) {
+        const int e = e0 + threadIdx.x;
+        if (e < entries) {
+            const int r = e / (int)p.Hkv, h = e - r * (int)p.Hkv;
+            const int j = (int)j0 + r;
+            const int32_t t = p.kept[b * p.kp_b + h * p.kp_h + j * p.kp_j];
+            const int32_t to = p.new_table[b * p.nt_b + (int64_t)(j / p.page) * p.nt_m];
+            k_from[threadIdx.x] = -1;
+            if (t >= 0 && to >= 0 && to < p.pages) {
+                const int64_t from = p.table[b * p.tb_b + (int64_t)(t / p.page) * p.tb_m];
+                const int fr = t % p.page, tr = j % p.page;
+                k_from[threadIdx.x] = from * p.k_g + fr * p.k_t + h * p.k_h;
+                k_to[threadIdx.x] = to * p.k_g + tr * p.k_t + h * p.k_h;
+                v_from[threadIdx.x] = from * p.v_g + fr * p.v_t + h * p.v_h;
+                v_to[threadIdx.x] = to * p.v_g + tr * p.v_t + h * p.v_h;
+            }
         }
+        __syncthreads();
+        const int here = entries - e0 < kCopy ? entries - e0 : kCopy;
+        W* const k = static_cast<W*>(p.k);
+        W* const v = static_cast<W*>(p.v);
+        const int64_t ks = VEC ? 1 : p.k_d, vs = VEC ? 1 : p.v_d;
+        // U pieces of the keys and of the values in flight per thread
+        constexpr int U = 4;
+        for (int i0 = threadIdx.x; i0 < here * pieces; i0 += U * kCopy) {
+            W kx[U], vx[U];
+            int64_t kt[U], vt[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kCopy;
+                const int row = i / pieces, d = (i - row * pieces) * per;
+                kt[u] = -1;
+                if (i < here * pieces && k_from[row] >= 0) {
+                    kx[u] = __ldcs(k + (k_from[row] + d * ks) / per);
+                    vx[u] = __ldcs(v + (v_from[row] + d * vs) / per);
+                    kt[u] = (k_to[row] + d * ks) / per;
+                    vt[u] = (v_to[row] + d * vs) / per;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (kt[u] >= 0) {
+                    __stcs(k + kt[u], kx[u]);
+                    __stcs(v + vt[u], vx[u]);
+                }
+        }
+        __syncthreads();
     }
 }
 
 }  // namespace
 
 int evict_select_block() { return kSelect; }
-int evict_copy_block() { return kCopy; }
+int64_t evict_copy_ctas(int64_t keep) { return (keep + kRows - 1) / kRows; }
 
-cudaError_t launch_evict(const EvictProblem& p, bool vec, int copy_grid, cudaStream_t s) {
-    evict_select_kernel<<<(unsigned)(p.Bn * p.Hkv), kSelect, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+cudaError_t launch_evict(const EvictProblem& p, bool vec, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (p.cap <= kCached) {
+        const int smem = (int)p.cap * 4;
+        auto* fn = evict_select_kernel<true>;
+        int per_sm = 0;
+        e = prepared_launch(
+            reinterpret_cast<const void*>(fn), smem > 40960 ? kCached * 4 : 40960, kSelect, &per_sm,
+            [&](int bytes) { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); },
+            [&](int* n) { *n = 1; return cudaSuccess; });
+        if (e != cudaSuccess) return e;
+        fn<<<(unsigned)(p.Bn * p.Hkv), kSelect, smem, s>>>(p);
+    } else {
+        evict_select_kernel<false><<<(unsigned)(p.Bn * p.Hkv), kSelect, 0, s>>>(p);
+    }
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (vec) evict_copy_kernel<true><<<copy_grid, kCopy, 0, s>>>(p);
-    else evict_copy_kernel<false><<<copy_grid, kCopy, 0, s>>>(p);
-    return cudaGetLastError();
+    // the copy may be launched while the selection still runs; it waits for its results
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.Bn * evict_copy_ctas(p.keep)));
+    cfg.blockDim = dim3(kCopy);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (vec) return cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint4, true>, p);
+    return p.es == 2 ? cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint16_t, false>, p)
+                     : cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint32_t, false>, p);
 }
 
 }  // namespace ssm

@@ -10,14 +10,16 @@
 //   linattn_generic_kernel  a prompt of any strides, types and sizes (N <= 256):
 //                           a warp carries 4 rows of S in registers over the
 //                           whole sequence.
-//   linattn_step_kernel     one token: S is read and written once, in 16-byte
-//                           vectors.
+//   linattn_step_bulk_kernel one token: S is read and written once, by bulk copies
+//                           through shared memory (rows without gaps).
+//   linattn_step_kernel     one token, rows of 16-byte vectors with gaps.
 //   linattn_step_generic_kernel  one token, any strides.
 //
 // The tensor-core form for prompts is linattn_chunk.cu.
 #include "../../include/ssm_causal.h"
 #include "common.cuh"
 #include "problem.h"
+#include "tma.cuh"
 
 namespace ssm {
 namespace {
@@ -241,6 +243,202 @@ __global__ void __launch_bounds__(kBlock) linattn_step_kernel(const LinAttnStepP
     }
 }
 
+// Dense rows: blocks of up to 16 KB of a head's state go through a ring of
+// stages in shared memory, brought in and taken out by bulk copies that one thread
+// issues; the CTA updates a stage in place.  Loads run kStages - 1 blocks ahead.  What else
+// an update reads is small but far away (the slot's index, then k, q, v and the decay),
+// so a CTA takes a unit of several blocks of one head, and reads the next unit's small
+// operands into registers while it works on this one.
+constexpr int kStageBytes = 16384, kStages = 3, kUnitRows = 512;
+struct BulkSmem {
+    alignas(128) unsigned char stage[kStages][kStageBytes];
+    uint64_t full[kStages];
+    int64_t slot[kStages];
+    float v[2][kUnitRows];
+};
+struct BulkShape {
+    uint32_t units;       // (b, h, group of blocks)
+    uint32_t groups;      // groups per head
+    int rows, blocks;     // rows per block, blocks per group
+};
+
+template <typename ST, int CPL>
+__global__ void __launch_bounds__(kBlock, 4) linattn_step_bulk_kernel(const LinAttnStepProblem p, const BulkShape sh,
+                                                                   DeviceError* err, long long wait_budget) {
+    constexpr int VE = Vec16<ST>::VE, VN = kUnitRows / kBlock, RU = StepShape<CPL>::RU;
+    extern __shared__ __align__(128) unsigned char raw[];
+    BulkSmem& sm = *reinterpret_cast<BulkSmem*>(raw);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nv = (int)(p.N / VE), lpr = step_lanes(nv), rows_at_once = 32 / lpr;
+    const int row_bytes = nv * 16, c0 = lane & (lpr - 1);
+    struct Unit {
+        int64_t b, h, row0;
+        int rows, blocks;
+    };
+    auto unit_at = [&](uint32_t u) {
+        Unit t;
+        const uint32_t head = u / sh.groups;
+        t.row0 = (int64_t)(u - head * sh.groups) * sh.rows * sh.blocks;
+        const int64_t left = p.P - t.row0;
+        t.rows = (int)(left < (int64_t)sh.rows * sh.blocks ? left : (int64_t)sh.rows * sh.blocks);
+        t.blocks = (t.rows + sh.rows - 1) / sh.rows;
+        t.b = head / (uint32_t)p.H;
+        t.h = head - (uint32_t)t.b * (uint32_t)p.H;
+        return t;
+    };
+    // thread 0: the copies, some blocks ahead of the work
+    uint32_t ahead_unit = blockIdx.x, issued = 0;
+    int ahead_block = 0;
+    Unit ahead;
+    int64_t ahead_slot = -1;
+    auto fetch = [&] {
+        if (ahead_unit >= sh.units) return;
+        if (ahead_block == 0) {
+            ahead = unit_at(ahead_unit);
+            ahead_slot = p.slot_idx ? p.slot_idx[ahead.b * p.ix_b] : ahead.b;
+            if (ahead_slot >= p.slots) ahead_slot = -1;
+        }
+        const int s = (int)(issued % kStages), r0 = ahead_block * sh.rows;
+        const int rows = ahead.rows - r0 < sh.rows ? ahead.rows - r0 : sh.rows;
+        const uint32_t bytes = ahead_slot < 0 ? 0u : (uint32_t)(rows * row_bytes);
+        sm.slot[s] = ahead_slot;
+        mbar_arrive_expect_tx(&sm.full[s], bytes);
+        if (bytes)
+            tma_load_1d(sm.stage[s], static_cast<const ST*>(p.s_in) + ahead_slot * p.si_b + ahead.h * p.si_h +
+                                         (ahead.row0 + r0) * p.si_p, bytes, &sm.full[s]);
+        ++issued;
+        if (++ahead_block == ahead.blocks) {
+            ahead_block = 0;
+            ahead_unit += gridDim.x;
+        }
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1);
+        mbar_fence_init();
+        for (int i = 0; i < kStages - 1; ++i) fetch();
+    }
+    // a unit's small operands
+    float kn[CPL][VE], qn[CPL][VE], vn[VN], gn = 0.0f;
+    auto load_small = [&](const Unit& t) {
+        const int64_t hk = t.h / (uint32_t)p.rep;
+        const int64_t kb = t.b * p.k_b + hk * p.k_h, qb = t.b * p.q_b + hk * p.q_h;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const int64_t n = (int64_t)(c0 + c * lpr) * VE + e;
+                const bool on = c0 + c * lpr < nv;
+                kn[c][e] = on ? ld_f(p.k, kb + n * p.k_n, p.io_dt) : 0.0f;
+                qn[c][e] = on ? ld_f(p.q, qb + n * p.q_n, p.io_dt) : 0.0f;
+            }
+#pragma unroll
+        for (int j = 0; j < VN; ++j) {
+            const int r = threadIdx.x + j * kBlock;
+            vn[j] = r < t.rows ? ld_f(p.v, t.b * p.v_b + t.h * p.v_h + (t.row0 + r) * p.v_p, p.io_dt) : 0.0f;
+        }
+        gn = p.g[t.b * p.g_b + t.h * p.g_h];
+    };
+    auto put_v = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < VN; ++j) sm.v[buf][threadIdx.x + j * kBlock] = vn[j];
+    };
+    uint32_t u = blockIdx.x, done = 0;
+    Unit next = unit_at(u < sh.units ? u : 0);
+    if (u < sh.units) {
+        load_small(next);
+        put_v(0);
+    }
+    __syncthreads();
+    bool ok = true;
+    for (int buf = 0; ok && u < sh.units; buf ^= 1) {
+        const Unit t = next;
+        float kf[CPL][VE], qf[CPL][VE];
+#pragma unroll
+        for (int c = 0; c < CPL; ++c)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) kf[c][e] = kn[c][e], qf[c][e] = qn[c][e];
+        const float lam = expf(decay_log(gn));
+        u += gridDim.x;
+        if (u < sh.units) {
+            next = unit_at(u);
+            load_small(next);
+        }
+        for (int blk = 0; blk < t.blocks; ++blk, ++done) {
+            const int s = (int)(done % kStages), r0 = blk * sh.rows;
+            const int rows = t.rows - r0 < sh.rows ? t.rows - r0 : sh.rows;
+            const bool here = mbar_wait_bounded(&sm.full[s], (done / kStages) & 1, wait_budget);
+            const int64_t slot = sm.slot[s];
+            if (here && slot >= 0) {
+                // RU groups of rows at a time: their loads together, their sums together
+                for (int g0 = warp * RU; g0 * rows_at_once < rows; g0 += RU * (kBlock / 32)) {
+                    float acc[RU];
+                    uint4 x[RU][CPL];
+#pragma unroll
+                    for (int r = 0; r < RU; ++r) {
+                        const int row = (g0 + r) * rows_at_once + lane / lpr;
+#pragma unroll
+                        for (int c = 0; c < CPL; ++c)
+                            if (row < rows && c0 + c * lpr < nv)
+                                x[r][c] = *(reinterpret_cast<const uint4*>(sm.stage[s] + row * row_bytes) + c0 + c * lpr);
+                    }
+#pragma unroll
+                    for (int r = 0; r < RU; ++r) {
+                        const int row = (g0 + r) * rows_at_once + lane / lpr;
+                        acc[r] = 0.0f;
+                        const float v = row < rows ? sm.v[buf][r0 + row] : 0.0f;
+#pragma unroll
+                        for (int c = 0; c < CPL; ++c)
+                            if (row < rows && c0 + c * lpr < nv) {
+                                float f[VE];
+                                Vec16<ST>::unpack(x[r][c], f);
+#pragma unroll
+                                for (int e = 0; e < VE; ++e) {
+                                    f[e] = fmaf(v, kf[c][e], lam * f[e]);
+                                    acc[r] = fmaf(f[e], qf[c][e], acc[r]);
+                                }
+                                *(reinterpret_cast<uint4*>(sm.stage[s] + row * row_bytes) + c0 + c * lpr) = Vec16<ST>::pack(f);
+                            }
+                    }
+                    const int64_t o0 = t.b * p.o_b + t.h * p.o_h + (t.row0 + r0) * p.o_p;
+                    if (lpr == 32) {
+                        const float sum = reduce_many<RU>(acc, lane);
+                        const int row = g0 + lane / (32 / RU);
+                        if (lane % (32 / RU) == 0 && row < rows) st_f(p.out, o0 + row * p.o_p, p.io_dt, sum * p.scale);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < RU; ++r) {
+                            for (int o = lpr >> 1; o >= 1; o >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
+                            const int row = (g0 + r) * rows_at_once + lane / lpr;
+                            if (c0 == 0 && row < rows) st_f(p.out, o0 + row * p.o_p, p.io_dt, acc[r] * p.scale);
+                        }
+                    }
+                }
+            }
+            if (blk + 1 == t.blocks && u < sh.units) put_v(buf ^ 1);
+            fence_proxy_async_smem();
+            if (__syncthreads_or(!here)) {
+                ok = false;
+                break;
+            }
+            if (threadIdx.x == 0) {
+                if (slot >= 0)
+                    tma_store_1d(static_cast<ST*>(p.s_out) + slot * p.so_b + t.h * p.so_h + (t.row0 + r0) * p.so_p,
+                                 sm.stage[s], (uint32_t)(rows * row_bytes));
+                bulk_commit();
+                bulk_wait_read<1>();  // the stage of the block before has been read out
+                fetch();
+            }
+        }
+    }
+    if (threadIdx.x == 0) {
+        if (!ok) {  // a copy never came: leave with none in flight
+            report_device_error(err, SSM_KERNEL_LINATTN_STEP_BULK, (long long)blockIdx.x);
+            for (; done < issued; ++done) mbar_wait_bounded(&sm.full[done % kStages], (done / kStages) & 1, wait_budget);
+        }
+        bulk_wait_all();
+    }
+}
+
 __global__ void __launch_bounds__(kBlock) linattn_step_generic_kernel(const LinAttnStepProblem p) {
     const int lane = threadIdx.x & 31;
     const int64_t nblk = (p.P + kBlock / 32 - 1) / (kBlock / 32);
@@ -272,6 +470,33 @@ cudaError_t step_t(const LinAttnStepProblem& p, int grid, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename ST, int CPL>
+cudaError_t bulk_t(const LinAttnStepProblem& p, int sms, int rows, DeviceError* err, long long budget, cudaStream_t s) {
+    auto* fn = linattn_step_bulk_kernel<ST, CPL>;
+    constexpr int smem = (int)sizeof(BulkSmem);
+    int per_sm = 0;
+    const cudaError_t e = prepared_launch(
+        reinterpret_cast<const void*>(fn), smem, kBlock, &per_sm,
+        [&](int bytes) { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); },
+        [&](int* n) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, fn, kBlock, smem); });
+    if (e != cudaSuccess) return e;
+    const int64_t wave = (int64_t)sms * (per_sm > 0 ? per_sm : 1), heads = p.Bn * p.H;
+    const int64_t per_head = (p.P + rows - 1) / rows;
+    // as many blocks per unit as leave every CTA four units or more
+    int64_t blocks = heads * per_head / (4 * wave);
+    blocks = blocks < 1 ? 1 : blocks;
+    blocks = blocks > per_head ? per_head : blocks;
+    if (blocks * rows > kUnitRows) blocks = kUnitRows / rows;
+    BulkShape sh;
+    sh.rows = rows;
+    sh.blocks = (int)blocks;
+    sh.groups = (uint32_t)((per_head + blocks - 1) / blocks);
+    sh.units = (uint32_t)(heads * sh.groups);
+    const int64_t grid = sh.units < wave ? sh.units : wave;
+    fn<<<(unsigned)grid, kBlock, smem, s>>>(p, sh, err, budget);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 int linattn_generic_block() { return kBlock; }
@@ -289,6 +514,21 @@ int linattn_step_rows(int st_dt, int64_t N, bool vec) {
     const int nv = (int)(N / (st_dt == kF32 ? 4 : 8));
     const int ru = nv <= 32 ? StepShape<1>::RU : StepShape<2>::RU;
     return (kBlock / 32) * ru * (32 / step_lanes(nv));
+}
+
+int linattn_step_bulk_rows(int st_dt, int64_t N) {
+    const int64_t rows = kStageBytes / (N * (st_dt == kF32 ? 4 : 2));
+    return (int)(rows < kUnitRows ? rows : kUnitRows);
+}
+
+cudaError_t launch_linattn_step_bulk(const LinAttnStepProblem& p, int sms, int dev, long long wait_budget, cudaStream_t s) {
+    DeviceError* err = device_error_ptr(dev);
+    if (!err) return cudaErrorUnknown;
+    const int rows = linattn_step_bulk_rows(p.st_dt, p.N);
+    if (p.st_dt == kF16) return bulk_t<__half, 1>(p, sms, rows, err, wait_budget, s);
+    if (p.st_dt == kBF16) return bulk_t<__nv_bfloat16, 1>(p, sms, rows, err, wait_budget, s);
+    return p.N <= 128 ? bulk_t<float, 1>(p, sms, rows, err, wait_budget, s)
+                      : bulk_t<float, 2>(p, sms, rows, err, wait_budget, s);
 }
 
 cudaError_t launch_linattn_step(const LinAttnStepProblem& p, int kernel, int grid, cudaStream_t s) {

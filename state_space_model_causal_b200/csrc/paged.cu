@@ -44,6 +44,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// Dependent launches: the join and the weights' kernel are launched while the one before
+// still runs (its CTAs need not have finished for theirs to start) and wait
+// here for its results.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------ work ranges --
 struct Range {
     int64_t total;   // tiles of all sequences
@@ -58,13 +64,24 @@ __device__ __forceinline__ int64_t seq_len(const PagedProblem& p, int64_t b) {
 __device__ __forceinline__ int64_t seq_tiles(const PagedProblem& p, int64_t b) {
     return (seq_len(p, b) + kTile - 1) / kTile;
 }
-__device__ __forceinline__ int64_t range_start(int64_t w, int64_t total, int64_t workers) {
-    return w * total / workers;  // tiles < 2^47, workers < 2^16: no overflow
-}
-// the worker whose range holds tile x
-__device__ __forceinline__ int64_t worker_of(int64_t x, int64_t total, int64_t workers) {
-    return ((x + 1) * workers - 1) / total;
-}
+// Equal ranges: the first `more` workers take one tile more than the others.
+struct Cut {
+    int64_t each, more;
+    __device__ __forceinline__ Cut(int64_t total, int64_t workers) {
+        if (total < ((int64_t)1 << 32)) {  // (a 64-bit division takes much longer)
+            each = (uint32_t)total / (uint32_t)workers;
+        } else {
+            each = total / workers;
+        }
+        more = total - each * workers;
+    }
+    __device__ __forceinline__ int64_t start(int64_t w) const { return w * each + (w < more ? w : more); }
+    // the worker whose range holds tile x
+    __device__ __forceinline__ int64_t worker_of(int64_t x) const {
+        const int64_t longer = more * (each + 1);
+        return x < longer ? x / (each + 1) : more + (x - longer) / each;
+    }
+};
 
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh) {
 #pragma unroll
@@ -86,8 +103,9 @@ __device__ Range find_range(const PagedProblem& p, int64_t worker) {
     int64_t mine = 0;
     for (int64_t b = threadIdx.x; b < p.Bn; b += kBlock) mine += seq_tiles(p, b);
     r.total = block_sum(mine, sh);
-    r.start = range_start(worker, r.total, p.workers);
-    r.end = range_start(worker + 1, r.total, p.workers);
+    const Cut cut(r.total, p.workers);
+    r.start = cut.start(worker);
+    r.end = cut.start(worker + 1);
     r.b = p.Bn;
     r.c = 0;
     if (r.start >= r.end) return r;
@@ -186,6 +204,7 @@ __device__ __forceinline__ void for_segments(const PagedProblem& p, Join<HPB, DP
     const int64_t hk = blockIdx.y / p.hblocks;
     const int hblk = (int)(blockIdx.y - hk * p.hblocks);
     const int heads = (int)(p.G - (int64_t)hblk * p.hpb < p.hpb ? p.G - (int64_t)hblk * p.hpb : p.hpb);
+    let_next_kernel_start();
     const Range r = find_range(p, worker);
     int64_t at = r.start, c = r.c;
     for (int64_t b = r.b; at < r.end; ++b) {
@@ -365,6 +384,7 @@ __device__ __forceinline__ uint32_t word(const uint4& u, int i) {
 template <typename T, int DP, bool WIDE>
 __global__ void __launch_bounds__(kBlock, WIDE ? 2 : 3) paged_mma_kernel(const PagedProblem p) {
     constexpr int HPB = WIDE ? 16 : 8, KI = DP / 32, VI = DP / 64;
+    constexpr int NB = DP == 64 && !WIDE ? 2 : 1;  // blocks of 16 tokens loaded together: 128 registers' worth
     constexpr int ROWS = WIDE ? 2 : 1;  // query rows per lane
     using M = Pack<T>;
     __shared__ Join<HPB, DP> sm;
@@ -394,105 +414,114 @@ __global__ void __launch_bounds__(kBlock, WIDE ? 2 : 3) paged_mma_kernel(const P
             m[w] = kNegInf;
             l[w] = 0.0f;
         }
-        // lane i < 16 looks after token t + i: its page, one block of tokens ahead
+        // lane i looks after token t + i: its page, one step ahead
         auto page_of = [&](int t) {
-            const int tok = t + (lane & 15);
+            const int tok = t + (lane & (16 * NB - 1));
             return tok < t1 ? table[(int64_t)((uint32_t)tok / (uint32_t)p.page) * p.tb_m] : -1;
         };
-        int32_t pg = page_of(t0 + warp * 16);
-        for (int t = t0 + warp * 16; t < t1; t += 16 * kWarps) {
-            const int tok = t + (lane & 15);
+        int32_t pg = page_of(t0 + warp * 16 * NB);
+        for (int t2 = t0 + warp * 16 * NB; t2 < t1; t2 += 16 * NB * kWarps) {
+            const int tok = t2 + (lane & (16 * NB - 1));
             const bool there = pg >= 0 && pg < p.pages;
             const int64_t row = (uint32_t)tok % (uint32_t)p.page;
             const int64_t ko = there ? pg * p.k_g + row * p.k_t : -1, vo = there ? pg * p.v_g + row * p.v_t : -1;
-            uint4 kf[2][KI], vf[4][VI];
-            bool on[4];
+            uint4 kf[NB][2][KI], vf[NB][4][VI];
+            bool on_all[NB][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int64_t at = shfl64(ko, r + 8 * j);
+            for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-                for (int i = 0; i < KI; ++i) {
-                    const int d = 32 * i + 8 * c;
-                    kf[j][i] = at >= 0 && d < p.D ? ld_stream16(kh + at + d) : zero;
-                }
-            }
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t at = shfl64(ko, 16 * nb + r + 8 * j);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t at = shfl64(vo, 2 * c + (j & 1) + 8 * (j >> 1));
-                on[j] = at >= 0;
-#pragma unroll
-                for (int i = 0; i < VI; ++i) {
-                    const int d = 64 * i + 8 * r;
-                    vf[j][i] = at >= 0 && d < p.D ? ld_stream16(vh + at + d) : zero;
-                }
-            }
-            pg = page_of(t + 16 * kWarps);
-
-            float s[2][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < KI; ++i) {
-                    M::mma(s[j], qf[0][i].x, WIDE ? qf[ROWS - 1][i].x : 0u, qf[0][i].y, WIDE ? qf[ROWS - 1][i].y : 0u,
-                           kf[j][i].x, kf[j][i].y);
-                    M::mma(s[j], qf[0][i].z, WIDE ? qf[ROWS - 1][i].z : 0u, qf[0][i].w, WIDE ? qf[ROWS - 1][i].w : 0u,
-                           kf[j][i].z, kf[j][i].w);
-                }
-            }
-            uint32_t a[4];
-            float f[ROWS];
-#pragma unroll
-            for (int w = 0; w < ROWS; ++w) {
-                float x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = on[j] ? s[j >> 1][2 * w + (j & 1)] * p.scale_log2 : kNegInf;
-                if (p.w && r + 8 * w < heads) {
-                    float* ws = p.ws_s + (b * p.Hq + hq0 + r + 8 * w) * p.cap;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int tk = t + 2 * c + (j & 1) + 8 * (j >> 1);
-                        if (tk < t1) ws[tk] = x[j];
+                    for (int i = 0; i < KI; ++i) {
+                        const int d = 32 * i + 8 * c;
+                        kf[nb][j][i] = at >= 0 && d < p.D ? ld_stream16(kh + at + d) : zero;
                     }
                 }
-                float mx = max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
-                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = max_nan(m[w], mx);
-                const float base = mn == kNegInf ? 0.0f : mn;  // no token yet: every weight is 0
-                f[w] = ex2_approx(m[w] - base);
-                m[w] = mn;
-                float e[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) e[j] = ex2_approx(x[j] - base + M::kLift);
-                l[w] = fmaf(l[w], f[w], (e[0] + e[1]) + (e[2] + e[3]));
-                a[w] = M::two(e[0], e[1]);
-                a[2 + w] = M::two(e[2], e[3]);
-                if (!WIDE) {
-                    const float2 h0 = M::back(a[0]), h1 = M::back(a[2]);
-                    a[1] = M::two(e[0] - h0.x, e[1] - h0.y);
-                    a[3] = M::two(e[2] - h1.x, e[3] - h1.y);
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t at = shfl64(vo, 16 * nb + 2 * c + (j & 1) + 8 * (j >> 1));
+                    on_all[nb][j] = at >= 0;
+#pragma unroll
+                    for (int i = 0; i < VI; ++i) {
+                        const int d = 64 * i + 8 * r;
+                        vf[nb][j][i] = at >= 0 && d < p.D ? ld_stream16(vh + at + d) : zero;
+                    }
                 }
             }
-            // the running maximum moves rarely
-            if (__any_sync(0xffffffffu, f[0] != 1.0f || f[ROWS - 1] != 1.0f)) {
+            pg = page_of(t2 + 16 * NB * kWarps);
 #pragma unroll
-                for (int j = 0; j < 8 * VI; ++j) {
-                    o[j][0] *= f[0];
-                    o[j][1] *= f[0];
-                    o[j][2] *= f[ROWS - 1];
-                    o[j][3] *= f[ROWS - 1];
+            for (int nb = 0; nb < NB; ++nb) {
+                const int t = t2 + 16 * nb;
+                const bool (&on)[4] = on_all[nb];
+                const uint4 (&kx)[2][KI] = kf[nb];
+                const uint4 (&vx)[4][VI] = vf[nb];
+                float s[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < KI; ++i) {
+                        M::mma(s[j], qf[0][i].x, WIDE ? qf[ROWS - 1][i].x : 0u, qf[0][i].y, WIDE ? qf[ROWS - 1][i].y : 0u,
+                               kx[j][i].x, kx[j][i].y);
+                        M::mma(s[j], qf[0][i].z, WIDE ? qf[ROWS - 1][i].z : 0u, qf[0][i].w, WIDE ? qf[ROWS - 1][i].w : 0u,
+                               kx[j][i].z, kx[j][i].w);
+                    }
                 }
+                uint32_t a[4];
+                float f[ROWS];
+#pragma unroll
+                for (int w = 0; w < ROWS; ++w) {
+                    float x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = on[j] ? s[j >> 1][2 * w + (j & 1)] * p.scale_log2 : kNegInf;
+                    if (p.w && r + 8 * w < heads) {
+                        float* ws = p.ws_s + (b * p.Hq + hq0 + r + 8 * w) * p.cap;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int tk = t + 2 * c + (j & 1) + 8 * (j >> 1);
+                            if (tk < t1) ws[tk] = x[j];
+                        }
+                    }
+                    float mx = max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
+                    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float mn = max_nan(m[w], mx);
+                    const float base = mn == kNegInf ? 0.0f : mn;  // no token yet: every weight is 0
+                    f[w] = ex2_approx(m[w] - base);
+                    m[w] = mn;
+                    float e[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) e[j] = ex2_approx(x[j] - base + M::kLift);
+                    l[w] = fmaf(l[w], f[w], (e[0] + e[1]) + (e[2] + e[3]));
+                    a[w] = M::two(e[0], e[1]);
+                    a[2 + w] = M::two(e[2], e[3]);
+                    if (!WIDE) {
+                        const float2 h0 = M::back(a[0]), h1 = M::back(a[2]);
+                        a[1] = M::two(e[0] - h0.x, e[1] - h0.y);
+                        a[3] = M::two(e[2] - h1.x, e[3] - h1.y);
+                    }
+                }
+                // the running maximum moves rarely
+                if (__any_sync(0xffffffffu, f[0] != 1.0f || f[ROWS - 1] != 1.0f)) {
+#pragma unroll
+                    for (int j = 0; j < 8 * VI; ++j) {
+                        o[j][0] *= f[0];
+                        o[j][1] *= f[0];
+                        o[j][2] *= f[ROWS - 1];
+                        o[j][3] *= f[ROWS - 1];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < VI; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
+                        const uint32_t b0 = __byte_perm(word(vx[0][i], j / 2), word(vx[1][i], j / 2), sel);
+                        const uint32_t b1 = __byte_perm(word(vx[2][i], j / 2), word(vx[3][i], j / 2), sel);
+                        M::mma(o[8 * i + j], a[0], a[1], a[2], a[3], b0, b1);
+                    }
             }
-#pragma unroll
-            for (int i = 0; i < VI; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
-                    const uint32_t b0 = __byte_perm(word(vf[0][i], j / 2), word(vf[1][i], j / 2), sel);
-                    const uint32_t b1 = __byte_perm(word(vf[2][i], j / 2), word(vf[3][i], j / 2), sel);
-                    M::mma(o[8 * i + j], a[0], a[1], a[2], a[3], b0, b1);
-                }
         }
 #pragma unroll
         for (int w = 0; w < ROWS; ++w) {
@@ -526,7 +555,10 @@ __global__ void __launch_bounds__(kBlock) paged_join_kernel(const PagedProblem p
     __shared__ int64_t sh[kWarps];
     __shared__ float red[kWarps];
     __shared__ float wgt[kBlock];
-    const int64_t b = blockIdx.x / p.Hq, hq = blockIdx.x - b * p.Hq;
+    __shared__ int64_t from[kBlock];
+    __shared__ float all[kWarps][256];
+    const int64_t b = blockIdx.x / (uint32_t)p.Hq, hq = blockIdx.x - b * p.Hq;
+    let_next_kernel_start();
     int64_t total = 0, c = 0;
     {
         int64_t mine = 0, before = 0;
@@ -542,6 +574,7 @@ __global__ void __launch_bounds__(kBlock) paged_join_kernel(const PagedProblem p
     const int64_t hk = hq / p.G, g = hq - hk * p.G;
     const int hblk = (int)(g / p.hpb), r = (int)(g - (int64_t)hblk * p.hpb);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    wait_for_previous_kernel();
     if (n == 0) {
         for (int64_t d = threadIdx.x; d < p.D; d += kBlock) st_f(p.out, b * p.o_b + hq * p.o_h + d * p.o_d, p.io_dt, 0.0f);
         if (threadIdx.x == 0) {
@@ -550,18 +583,13 @@ __global__ void __launch_bounds__(kBlock) paged_join_kernel(const PagedProblem p
         }
         return;
     }
-    const int64_t w0 = worker_of(c, total, p.workers), w1 = worker_of(c + n - 1, total, p.workers);
+    const Cut cut(total, p.workers);
+    const int64_t w0 = cut.worker_of(c), w1 = cut.worker_of(c + n - 1);
     if (w0 == w1) return;  // written whole
-    auto entry = [&](int64_t w) {
-        return part_of(p, w, hk, hblk, range_start(w, total, p.workers) >= c ? 0 : 1) * p.hpb + r;
-    };
-    // An empty range (fewer tiles than workers) holds no part.
-    auto holds = [&](int64_t w) {
-        return range_start(w, total, p.workers) < range_start(w + 1, total, p.workers);
-    };
+    // every range between them holds a part (none is empty: its neighbours are not)
+    auto entry = [&](int64_t w) { return part_of(p, w, hk, hblk, cut.start(w) >= c ? 0 : 1) * p.hpb + r; };
     float m = kNegInf;
-    for (int64_t w = w0 + threadIdx.x; w <= w1; w += kBlock)
-        if (holds(w)) m = max_nan(m, p.ws_ml[entry(w)].x);
+    for (int64_t w = w0 + threadIdx.x; w <= w1; w += kBlock) m = max_nan(m, p.ws_ml[entry(w)].x);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) red[warp] = m;
@@ -569,43 +597,56 @@ __global__ void __launch_bounds__(kBlock) paged_join_kernel(const PagedProblem p
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) m = max_nan(m, red[i]);
     __syncthreads();
-    float l = 0.0f, acc[2] = {0.0f, 0.0f};  // this thread's elements d = threadIdx.x, + 128
+    // warp by warp, every fourth part; a lane takes elements lane, lane + 32, ...
+    float l = 0.0f, acc[8] = {};
+    const int de = (int)(p.D + 31) / 32;
     for (int64_t base = w0; base <= w1; base += kBlock) {
         const int64_t w = base + threadIdx.x;
-        float f = 0.0f;
-        if (w <= w1 && holds(w)) {
-            const float2 ml = p.ws_ml[entry(w)];
+        if (w <= w1) {
+            const int64_t e = entry(w);
+            const float2 ml = p.ws_ml[e];
+            float f = 0.0f;
             if (ml.x != kNegInf) {
                 f = exp2f(ml.x - m);
                 l = fmaf(f, ml.y, l);
             }
+            wgt[threadIdx.x] = f;
+            from[threadIdx.x] = e * p.D;
         }
-        wgt[threadIdx.x] = f;
         __syncthreads();
         const int cnt = (int)(w1 - base + 1 < kBlock ? w1 - base + 1 : kBlock);
-#pragma unroll 4
-        for (int i = 0; i < cnt; ++i) {
-            const float fi = wgt[i];
-            if (fi != 0.0f) {  // (a NaN counts)
-                const float* o = p.ws_o + entry(base + i) * p.D;
+        for (int i = warp; i < cnt; i += 4 * kWarps) {
+            float fi[4], v[4][8];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (threadIdx.x + e * kBlock < p.D) acc[e] = fmaf(fi, o[threadIdx.x + e * kBlock], acc[e]);
+            for (int u = 0; u < 4; ++u) {  // 4 parts in flight
+                const int at = i + u * kWarps;
+                fi[u] = at < cnt ? wgt[at] : 0.0f;
+                const float* o = p.ws_o + from[at < cnt ? at : i];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[u][e] = e < de && lane + 32 * e < p.D ? o[lane + 32 * e] : 0.0f;
             }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = fi[u] != 0.0f ? fmaf(fi[u], v[u][e], acc[e]) : acc[e];  // (a NaN counts)
         }
         __syncthreads();
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) red[warp] = l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < de) all[warp][lane + 32 * e] = acc[e];
     __syncthreads();
     l = 0.0f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) l += red[i];
+    for (int d = threadIdx.x; d < p.D; d += kBlock) {
+        float sum = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int64_t d = threadIdx.x + e * kBlock;
-        if (d < p.D) st_f(p.out, b * p.o_b + hq * p.o_h + d * p.o_d, p.io_dt, m == kNegInf ? 0.0f : acc[e] / l);
+        for (int i = 0; i < kWarps; ++i) sum += all[i][d];
+        st_f(p.out, b * p.o_b + hq * p.o_h + d * p.o_d, p.io_dt, m == kNegInf ? 0.0f : sum / l);
     }
     if (threadIdx.x == 0) {
         const float lse2 = m == kNegInf ? kNegInf : m + log2f(l);
@@ -623,6 +664,7 @@ __global__ void __launch_bounds__(kBlock) paged_weights_kernel(const PagedProble
     const int64_t len = seq_len(p, b);
     const int64_t t0 = (blockIdx.x - row * blocks) * kWeightTokens;
     const int64_t t1 = t0 + kWeightTokens < len ? t0 + kWeightTokens : len;
+    wait_for_previous_kernel();
     for (int64_t t = t0 + threadIdx.x; t < t1; t += kBlock) {
         float sum = 0.0f;
         for (int64_t g = 0; g < p.G; ++g) {
@@ -632,6 +674,20 @@ __global__ void __launch_bounds__(kBlock) paged_weights_kernel(const PagedProble
         }
         p.w_out[b * p.wo_b + hk * p.wo_h + t * p.wo_t] = p.w[b * p.w_b + hk * p.w_h + t * p.w_t] + sum;
     }
+}
+
+// a launch that may start before the stream's last kernel has finished
+cudaError_t launch_after(void (*fn)(const PagedProblem), unsigned grid, const PagedProblem& p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kBlock);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 template <typename T>
@@ -675,11 +731,9 @@ cudaError_t launch_paged(const PagedProblem& p, int kernel, cudaStream_t s) {
     else generic_t<float>(p, grid, s);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    paged_join_kernel<<<(unsigned)(p.Bn * p.Hq), kBlock, 0, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_after(paged_join_kernel, (unsigned)(p.Bn * p.Hq), p, s);
     if (e != cudaSuccess || !p.w || p.cap == 0) return e;
-    paged_weights_kernel<<<(unsigned)(paged_weight_blocks(p.cap) * p.Bn * p.Hkv), kBlock, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_after(paged_weights_kernel, (unsigned)(paged_weight_blocks(p.cap) * p.Bn * p.Hkv), p, s);
 }
 
 }  // namespace ssm

@@ -346,6 +346,8 @@ uint64_t linattn_chunk_record_bytes();    // one state of a CTA
 cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, int pieces, int64_t per_piece, float* rec,
                                  double* rec_g, long long wait_budget, int dev, cudaStream_t s);
 cudaError_t launch_linattn_step(const LinAttnStepProblem& p, int kernel, int grid, cudaStream_t s);
+int linattn_step_bulk_rows(int st_dt, int64_t N);  // rows of the state per item of the bulk-copy kernel
+cudaError_t launch_linattn_step_bulk(const LinAttnStepProblem& p, int sms, int dev, long long wait_budget, cudaStream_t s);
 int linattn_step_block();
 int linattn_step_rows(int st_dt, int64_t N, bool vec);  // rows of the state per CTA
 cudaError_t launch_paged(const PagedProblem& p, int kernel, cudaStream_t s);
@@ -353,9 +355,9 @@ int paged_block();
 int64_t paged_weight_blocks(int64_t cap);  // CTAs per (sequence, key-value head) of the weights' kernel
 int paged_heads_per_cta(int kernel, int64_t G);
 int paged_ctas_per_sm(int kernel, int64_t G, int64_t D);
-cudaError_t launch_evict(const EvictProblem& p, bool vec, int copy_grid, cudaStream_t s);
+cudaError_t launch_evict(const EvictProblem& p, bool vec, cudaStream_t s);
 int evict_select_block();
-int evict_copy_block();
+int64_t evict_copy_ctas(int64_t keep);  // CTAs of the copy per sequence
 cudaError_t launch_delta_sum(const DeltaSumProblem& p, int grid, int block, cudaStream_t s);
 cudaError_t launch_carry_fold(const CarryFoldProblem& p, int grid, int block, cudaStream_t s);
 int scan_m2_rows_per_cta(int64_t N);
