@@ -149,13 +149,20 @@ ssm_status linattn_impl(const ssm_linattn_args* a, cudaStream_t stream, uint64_t
         const int64_t units = B * H * ((P + linattn_chunk_values() - 1) / linattn_chunk_values());
         const int64_t chunks = (L + linattn_chunk_tokens() - 1) / linattn_chunk_tokens();
         const int dev = current_device(dry);
-        // with less than half a wave of CTAs, each sequence in pieces
-        int64_t pieces = std::min<int64_t>(sm_count(dry, dev) / units, chunks / 2);
-        if (pieces < 2 || (!ws_query && !a->workspace)) pieces = 1;
-        int64_t per_piece = (chunks + pieces - 1) / pieces;
-        pieces = (chunks + per_piece - 1) / per_piece;
-        const uint64_t rec = pieces > 1 ? round256((uint64_t)units * pieces * linattn_chunk_record_bytes()) : 0;
-        const uint64_t need = pieces > 1 ? rec + round256((uint64_t)units * pieces * 8) : 0;
+        // With half a wave of CTAs or less, each sequence in pieces: `others` after the
+        // first, which is half as long; each launch computes `others` pieces at a time.
+        // (Two launches of fewer than 6 chunks each would take longer than one of 12.)
+        int64_t others = std::min<int64_t>(sm_count(dry, dev) / units, chunks / 2);
+        if (others < 2 || chunks < 12 || (!ws_query && !a->workspace)) others = 0;
+        LinAttnPieces cut{1, chunks, 0};
+        if (others) {
+            cut.per_piece = (2 * chunks + 2 * others) / (2 * others + 1);  // about chunks / (others + 1/2), rounded up
+            cut.piece0 = std::max<int64_t>(1, chunks - others * cut.per_piece);
+            cut.pieces = (int)(1 + (chunks - cut.piece0 + cut.per_piece - 1) / cut.per_piece);
+        }
+        const int64_t pieces = cut.pieces;
+        const uint64_t rec = pieces > 1 ? round256((uint64_t)units * (pieces - 1) * linattn_chunk_record_bytes()) : 0;
+        const uint64_t need = pieces > 1 ? rec + round256((uint64_t)units * (pieces - 1) * 8) : 0;
         if (ws_query) {
             *ws_query = need;
             return SSM_OK;
@@ -167,11 +174,11 @@ ssm_status linattn_impl(const ssm_linattn_args* a, cudaStream_t stream, uint64_t
                 if (present(*t) && overlap(ws, *t)) return SSM_ERR_ALIAS;
         }
         if (units > INT32_MAX / pieces) return SSM_ERR_UNSUPPORTED;
-        fill_info(a->info, SSM_KERNEL_LINATTN_CHUNK, (int)(units * pieces), linattn_chunk_block(), linattn_chunk_smem(),
+        fill_info(a->info, SSM_KERNEL_LINATTN_CHUNK, (int)(units * std::max<int64_t>(pieces - 1, 1)), linattn_chunk_block(), linattn_chunk_smem(),
                   linattn_chunk_values(), units * pieces);
         if (dry) return SSM_OK;
         char* ws = static_cast<char*>(a->workspace);
-        return launch_linattn_chunk(p, units, (int)pieces, per_piece, reinterpret_cast<float*>(ws),
+        return launch_linattn_chunk(p, units, cut, reinterpret_cast<float*>(ws),
                                     reinterpret_cast<double*>(ws + rec), kWaitBudget, dev, stream) == cudaSuccess
                    ? SSM_OK : SSM_ERR_CUDA;
     }

@@ -15,18 +15,19 @@
 // is being finished.
 //
 // A CTA takes one (batch, head, 64 values) and a run of chunks; the keys' size
-// is padded to 128 by the loads (zeros).  16 warps:
+// is padded to 128 by the loads (zeros).  20 warps:
 //   0      loads Q, K, V tiles by TMA, two chunks deep
-//   1      issues the products (one thread)
+//   1, 3   issue the products (one thread each): P V and Q K^T, and those with the state
 //   2      the chunk's sums G, in double, stored as a float and its remainder:
 //          differences of two sums keep float accuracy however large the sums
-//   3      allocates tensor memory
-//   4-7    scores: tensor memory -> exp(G_t - G_s), mask -> 16 bits -> tensor memory
-//          (in place).  With R the sum at the end of s's 32 tokens, exp(G_t - G_s) =
+//   4-7    scores: tensor memory -> exp(G_t - G_s), mask -> 16 bits -> tensor memory.
+//          With R the sum at the end of s's 32 tokens, exp(G_t - G_s) =
 //          exp(G_t - R) exp(R - G_s), a factor per row and one per column; an exponential
-//          per element only where the 32 tokens of the diagonal decay by more than 2^100
+//          per element only where the 32 tokens of the diagonal decay by more than 2^100.
+//          These warps take the diagonal block of 32 columns and the one before it
 //   8-11   the state: float32 in registers (lane = key, 64 values)
-//   12-15  V~ of the next chunk, then the output of this one
+//   12-15  V~
+//   16-19  the scores' other blocks, then the output
 //
 // Precision.  Accumulators and S are float32.  V~ is given to the tensor cores as
 // two 16-bit numbers, the second holding what rounding the first left over (16
@@ -35,9 +36,10 @@
 // rounded once, as the output will be.  For f16, whose range is small, a power of two is taken out of every row of
 // scores, of V~ and of S, and put back in float32: it costs three maxima.
 //
-// Few long sequences: with less than one CTA per SM, each is cut into pieces of
-// chunks.  A first launch computes every piece's end state from zero (keys and
-// values only), a second starts every piece from the states composed of those.
+// Few long sequences: with half a CTA per SM or less, each is cut into pieces of
+// chunks.  A first launch computes piece 0, and of the others but the last the end
+// states from zero (keys and values only, which takes half as long: piece 0 is half as
+// long as the others); a second starts pieces 1, 2, ... from the states composed of those.
 #include <type_traits>
 
 #include "../../include/ssm_causal.h"
@@ -48,7 +50,7 @@
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int C = 128;        // tokens per chunk
 constexpr int DV = 64;        // values per CTA
 constexpr int kBlockBytes = C * 128;               // a tile: 128 rows of 64 16-bit elements
@@ -60,13 +62,14 @@ constexpr int kTiles = kOffS + kBlockBytes;        // 212,992 bytes
 struct Small {
     uint64_t full_qk[2], full_v[2], empty_qk[2], empty_v[2];  // loads
     uint64_t g_full[2], g_empty[2];                           // decay sums
-    uint64_t sc_full[2];                                      // scores' accumulators
+    uint64_t sc_full, top_full;                               // scores' accumulator; f16: their largest
     uint64_t p_full, vt_full, kv_full, kv_empty, s_full, qs_done, o_full, o_empty, red_full[2], spare;
     uint32_t tmem;
     int abort;
     uint8_t red[2][2][4];      // f16: exponents of the largest values, per warp
     int s_lift[2], v_lift[2];  // f16: S, V~ were divided by 2^lift
     int8_t row_lift[2][C];     // f16: so was a row of scores
+    uint8_t row_top[2][C];     // f16: exponent of a row's largest score, of either group
     alignas(16) float g_hi[2][C], column[2][C];  // read as vectors
     __half g_lo[2][C];         // remainder of g_hi, below 2^-24 of it
 };
@@ -75,27 +78,23 @@ static_assert(kSmem <= 232448, "shared memory of one CTA");
 static_assert(kTiles % 16 == 0, "alignment of the vectors behind the tiles");
 
 // tensor memory columns
-// (the weights P take the first 64 of their scores' 128 columns)
-constexpr uint32_t kSc = 0, kOa = 256, kOb = 320, kKv = 384, kColumns = 512;
+constexpr uint32_t kSc = 0, kP = 128, kOa = 192, kOb = 256, kKv = 320, kColumns = 512;
 
 struct ChunkArgs {
     LinAttnProblem p;
     int64_t pt;          // ceil(P / 64)
-    int64_t chunks;      // ceil(L / 128)
     int pieces;          // pieces per sequence
-    int64_t per_piece;   // chunks per piece
-    int states_only;     // first of two launches
+    int64_t piece0, per_piece;  // chunks of piece 0, and of the others
+    int phase;           // 0: one launch, 1: pieces 0 .. pieces - 2, 2: pieces 1 .. pieces - 1
     int out32;           // rows of out are whole, aligned 32-byte sectors
-    float* rec;          // [unit][S_0, ends of pieces 0 .. pieces - 2][64 values][128 keys]
-    double* rec_g;       // [unit][pieces]: log2 of the piece's decay
+    float* rec;          // [unit][pieces - 1][64 values][128 keys]: end of the piece (from zero, but for 0)
+    double* rec_g;       // [unit][pieces - 1]: log2 of the piece's decay
     DeviceError* err;
     long long wait_budget;
 };
 
-// Bounded wait; a wait that runs out ends every role of the CTA.  The part that
-// spins is out of line: the warps' code has to stay in the instruction cache
-// (see the note on code size at the kernel).
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* abort, DeviceError* err, long long budget) {
+// Bounded wait; a wait that runs out ends every role of the CTA.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* abort, DeviceError* err, long long budget) {
     const long long t0 = clock64();
     for (;;) {
         if (mbar_try(bar, parity)) return true;
@@ -167,7 +166,20 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
                  : "memory");
 }
 
-// Code size: 16 warps run a dozen different loops, each once per chunk.  Unrolled
+// Registers per thread: 96 at launch (640 threads), of which the warpgroup that holds the
+// state takes 128 and the others keep 88.
+constexpr int kRegs = 88, kRegsState = 128;
+static_assert(4 * kRegs + kRegsState <= 5 * 96, "no more than the launch has");
+template <int R>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// Code size: 20 warps run a dozen different loops, each once per chunk.  Unrolled
 // throughout, they did not fit the instruction caches, and warps waited for
 // instructions more than for anything else (10 of 26 stalled warps per issue; 237 us
 // for 4 x 2048 tokens of 32 heads of 128).  So loops over blocks of 32 columns stay loops.
@@ -180,12 +192,12 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     Small& sm = *reinterpret_cast<Small*>(smem + kTiles);
     const LinAttnProblem& p = a.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int n_pieces = a.states_only ? a.pieces - 1 : a.pieces;
+    const int n_pieces = a.phase == 0 ? 1 : a.pieces - 1;
     const int64_t unit = blockIdx.x / n_pieces;
-    const int piece = (int)(blockIdx.x - unit * n_pieces);
+    const int piece = (int)(blockIdx.x - unit * n_pieces) + (a.phase == 2 ? 1 : 0);
     const int64_t bh = unit / a.pt, b = bh / p.H, h = bh - b * p.H;
     const int p0 = (int)(unit - bh * a.pt) * DV;
-    const bool outputs = !a.states_only;
+    const bool outputs = a.phase != 1 || piece == 0;
 
     int64_t len = p.L;
     if (p.lens) {
@@ -193,8 +205,8 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         len = n < 0 ? 0 : (n < p.L ? n : p.L);
     }
     const int64_t seq_chunks = (len + C - 1) / C;
-    const int64_t c0 = piece * a.per_piece;
-    int64_t c1 = c0 + a.per_piece;
+    const int64_t c0 = piece == 0 ? 0 : a.piece0 + (piece - 1) * a.per_piece;
+    int64_t c1 = piece == 0 ? a.piece0 : c0 + a.per_piece;
     if (c1 > seq_chunks) c1 = seq_chunks;
     const int n = c1 > c0 ? (int)(c1 - c0) : 0;  // this CTA's chunks
 
@@ -202,23 +214,24 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.full_qk[i], 1);
             mbar_init(&sm.full_v[i], 1);
-            mbar_init(&sm.empty_qk[i], 1);
-            mbar_init(&sm.empty_v[i], 1);
+            mbar_init(&sm.empty_qk[i], outputs ? 2 : 1);  // both issuers
+            mbar_init(&sm.empty_v[i], 5);                 // an issuer, and the warps that make V~
             mbar_init(&sm.g_full[i], 1);
-            mbar_init(&sm.g_empty[i], outputs ? 12 : 8);
-            mbar_init(&sm.sc_full[i], 1);
+            mbar_init(&sm.g_empty[i], outputs ? 16 : 8);
         }
-        mbar_init(&sm.p_full, 4);
+        mbar_init(&sm.sc_full, 1);
+        mbar_init(&sm.top_full, 8);
+        mbar_init(&sm.p_full, 8);
         mbar_init(&sm.vt_full, 4);
         mbar_init(&sm.kv_full, 1);
         mbar_init(&sm.kv_empty, 4);
         mbar_init(&sm.s_full, 4);
         mbar_init(&sm.qs_done, 1);
-        mbar_init(&sm.o_full, 1);
+        mbar_init(&sm.o_full, 2);
         mbar_init(&sm.o_empty, 4);
         mbar_init(&sm.red_full[0], 4);
         mbar_init(&sm.red_full[1], 4);
-        mbar_init(&sm.spare, 1);
+        mbar_init(&sm.spare, outputs ? 2 : 1);
         sm.abort = (smem_u32(smem) & 1023u) != 0;  // the swizzle counts from 1024-byte boundaries
         if (sm.abort) report_device_error(a.err, SSM_KERNEL_LINATTN_CHUNK, (long long)blockIdx.x);
         mbar_fence_init();
@@ -252,6 +265,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         return true;
     };
 
+    if (warp < 4) fewer_registers<kRegs>();
     if (warp == 0) {
         // ------------------------------------------------------------- loads --
         if (lane == 0 && start) {
@@ -282,61 +296,65 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                     mbar_wait_bounded(&sm.full_v[i & 1], (i >> 1) & 1, a.wait_budget);
                 }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
         // ---------------------------------------------------------- products --
-        if (start && n > 0) {
-            constexpr uint32_t d_qk = mma_desc(HT::kType, false, false, 128, 128);
-            constexpr uint32_t d_pv = mma_desc(HT::kType, false, true, 128, DV);
-            constexpr uint32_t d_kv = mma_desc(HT::kType, true, true, 128, 2 * DV);
-            const uint32_t base = smem_u32(smem);
-            const uint64_t vt = tile_desc(base + kOffVt, kBlockBytes), st = tile_desc(base + kOffS, kBlockBytes);
-            auto qd = [&](int s) { return tile_desc(base + s * kStageBytes, kBlockBytes); };
-            auto kd = [&](int s) { return tile_desc(base + s * kStageBytes + 2 * kBlockBytes, kBlockBytes); };
-            auto vd = [&](int s) { return tile_desc(base + s * kStageBytes + 4 * kBlockBytes, kBlockBytes); };
-            // Order: P V of a chunk, the scores of the next, then its two products with the
-            // state.  The output of the first is read while the second runs, the weights
-            // are made while the last two run, the state is brought up to date during the
-            // first two, and a stage is refilled two steps after it was last read.
-            constexpr int kTile = kBlockBytes >> 4, kRows = 2048 >> 4;  // to the next 64 elements, 16 rows
-            bool ok = true;
-            for (int i = -1; ok && i < n; ++i) {
+        // Two warps, so that the products of one can be issued while the other waits
+        // for operands: the weights are made while the products with the state run, the
+        // state is brought up to date during the others, and a stage is refilled two
+        // steps after it was last read.
+        constexpr uint32_t d_qk = mma_desc(HT::kType, false, false, 128, 128);
+        constexpr uint32_t d_pv = mma_desc(HT::kType, false, true, 128, DV);
+        constexpr uint32_t d_kv = mma_desc(HT::kType, true, true, 128, 2 * DV);
+        constexpr int kTile = kBlockBytes >> 4, kRows = 2048 >> 4;  // to the next 64 elements, 16 rows
+        const uint32_t base = smem_u32(smem);
+        auto qd = [&](int s) { return tile_desc(base + s * kStageBytes, kBlockBytes); };
+        auto kd = [&](int s) { return tile_desc(base + s * kStageBytes + 2 * kBlockBytes, kBlockBytes); };
+        auto vd = [&](int s) { return tile_desc(base + s * kStageBytes + 4 * kBlockBytes, kBlockBytes); };
+        if (warp == 1 && start && outputs && n > 0) {
+            for (int i = -1; i < n; ++i) {
                 const int s = i & 1, j = i + 1, js = j & 1;
-                const uint32_t ph = (i >> 1) & 1, jph = (j >> 1) & 1;
-                if (outputs) {
-                    if (i >= 0) {
-                        ok = wait(&sm.p_full, i & 1) && wait(&sm.full_v[s], ph);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vs = vd(s);
-                        product_ts<kRows>(tm + kOa, tm + kSc + s * 128, vs, d_pv);
-                        mma_commit(&sm.o_full);
-                        mma_commit(&sm.empty_v[s]);
-                    }
-                    if (j == n) break;
-                    // (the columns held the weights of the chunk before this one's: their
-                    // products were over when that chunk's output was read)
-                    ok = wait(&sm.full_qk[js], jph);
-                    if (!ok) break;
+                if (i >= 0) {
+                    // (V~ made: rows behind the end are 0 by then, in V too)
+                    if (!wait(&sm.full_v[s], (i >> 1) & 1) || !wait(&sm.vt_full, i & 1) || !wait(&sm.p_full, i & 1) ||
+                        (i > 0 && !wait(&sm.o_empty, (i - 1) & 1)))
+                        break;
                     tc_fence_after();
-                    const uint64_t qs = qd(js), ks = kd(js);
-                    product_ss<2, kTile - 6, 2, kTile - 6>(tm + kSc + js * 128, qs, ks, d_qk);
-                    mma_commit(&sm.sc_full[js]);
+                    product_ts<kRows>(tm + kOa, tm + kP, vd(s), d_pv);
+                    mma_commit(&sm.o_full);
+                    mma_commit(&sm.empty_v[s]);
                 }
-                if (j == n) break;
-                // K^T [V~ high | V~ low] (side by side, added up by the state's warps) and Q S
-                ok = wait(&sm.vt_full, j & 1) && wait(&sm.full_qk[js], jph) && (j == 0 || wait(&sm.kv_empty, i & 1)) &&
-                     (!outputs || (wait(&sm.s_full, j & 1) && (j == 0 || wait(&sm.o_empty, i & 1))));
-                if (!ok) break;
+                // the scores of the next chunk (the last ones were read when their weights were ready)
+                if (j == n || !wait(&sm.full_qk[js], (j >> 1) & 1)) break;
                 tc_fence_after();
-                const uint64_t ks = kd(js), qs = qd(js);
-                product_ss<kRows, kRows, kRows, kRows>(tm + kKv, ks, vt, d_kv);
-                product_ss<2, kTile - 6, kRows, kRows>(tm + kOb, qs, st, d_pv, outputs);
-                mma_commit(&sm.kv_full);
-                mma_commit(&sm.qs_done);
+                product_ss<2, kTile - 6, 2, kTile - 6>(tm + kSc, qd(js), kd(js), d_qk);
+                mma_commit(&sm.sc_full);
                 mma_commit(&sm.empty_qk[js]);
-                if (!outputs) mma_commit(&sm.empty_v[js]);
             }
-            // every product done before tensor memory is freed
+        } else if (warp == 3 && start) {
+            const uint64_t vt = tile_desc(base + kOffVt, kBlockBytes), st = tile_desc(base + kOffS, kBlockBytes);
+            for (int i = 0; i < n; ++i) {
+                const int s = i & 1;
+                // K^T [V~ high | V~ low] (side by side, added up by the state's warps) and Q S
+                if (!wait(&sm.vt_full, i & 1) || !wait(&sm.full_qk[s], (i >> 1) & 1) ||
+                    (i > 0 && !wait(&sm.kv_empty, (i - 1) & 1)))
+                    break;
+                tc_fence_after();
+                product_ss<kRows, kRows, kRows, kRows>(tm + kKv, kd(s), vt, d_kv);
+                mma_commit(&sm.kv_full);
+                if (outputs) {
+                    if (!wait(&sm.s_full, i & 1) || (i > 0 && !wait(&sm.o_empty, (i - 1) & 1))) break;
+                    tc_fence_after();
+                    product_ss<2, kTile - 6, kRows, kRows>(tm + kOb, qd(s), st, d_pv);
+                    mma_commit(&sm.qs_done);
+                    mma_commit(&sm.o_full);
+                } else {
+                    mma_commit(&sm.empty_v[s]);
+                }
+                mma_commit(&sm.empty_qk[s]);
+            }
+        }
+        // every product done before tensor memory is freed
+        if (start && n > 0 && (warp == 3 || outputs)) {
             mma_commit(&sm.spare);
             mbar_wait_bounded(&sm.spare, 0, a.wait_budget);
         }
@@ -381,45 +399,87 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.g_full[s]);
         }
-    } else if (warp >= 4 && warp < 8) {
-        // ------------------------------------------------------------ scores --
-        const int w = warp & 3, row = w * 32 + lane;
+    } else if ((warp >= 4 && warp < 8) || warp >= 16) {
+        // ------------------------------------------------- scores and output --
+        fewer_registers<kRegs>();
+        const int w = warp & 3, row = w * 32 + lane, group = warp >= 16;
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
+        // blocks of 32 columns: the diagonal and the one before it, or those before them
+        const int split = w > 1 ? w - 1 : w, first = group ? 0 : split, last = group ? split : w + 1;
+        T* const out = static_cast<T*>(p.out) + b * p.o_b + h * p.o_h + p0;
+        auto output = [&](int i, float across) {  // across: scale exp(G_t)
+            if (!wait(&sm.o_full, i & 1)) return false;
+            tc_fence_after();
+            float inside = p.scale, over = across;
+            if (HT::kScaled) {
+                over *= pow2(sm.s_lift[i & 1]);
+                inside *= pow2(sm.row_lift[i & 1][row]);
+            }
+            const int64_t t = (c0 + i) * C + row;
+            T* const orow = out + t * p.o_t;
+            const u64 over2 = pk(over, over), inside2 = pk(inside, inside);
+#pragma unroll 1
+            for (int g = 0; g < DV; g += 16) {
+                uint32_t x[16], y[16], o[8];
+                tmem_ld16x2(tm + lanes + kOa + g, tm + lanes + kOb + g, x, y);
+                if (g == DV - 16) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.o_empty);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    float f0, f1;
+                    upk(ffma2(pk(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), over2,
+                              fmul2(pk(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), inside2)), f0, f1);
+                    o[j / 2] = HT::two(f0, f1);
+                }
+                if (t < len && p0 + g < p.P) {
+                    if (a.out32) {  // a whole 32-byte sector
+                        store32(orow + g, o);
+                    } else {
+                        *reinterpret_cast<uint4*>(orow + g) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (p0 + g + 8 < p.P) *reinterpret_cast<uint4*>(orow + g + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+            }
+            return true;
+        };
         for (int i = 0; start && outputs && i < n; ++i) {
             const int s = i & 1;
-            const uint32_t ph = (i >> 1) & 1;
-            if (!wait(&sm.g_full[s], ph)) break;
+            if (!wait(&sm.g_full[s], (i >> 1) & 1)) break;
             const float hi = sm.g_hi[s][row], lo = __half2float(sm.g_lo[s][row]);
-            if (!wait(&sm.sc_full[s], ph)) break;
+            if (!wait(&sm.sc_full, i & 1)) break;
             tc_fence_after();
-            const uint32_t sc = tm + lanes + kSc + s * 128;
+            const uint32_t sc = tm + lanes + kSc, pw = tm + lanes + kP;
             float lower = 1.0f;
             if (HT::kScaled) {
                 float mx = 0.0f;
 #pragma unroll 1
-                for (int g = 0; g <= w; ++g) {
+                for (int g = first; g < last; ++g) {
                     uint32_t r[32];
                     tmem_ld32(sc + g * 32, r);
-                    const int last = g < w ? 31 : lane;
+                    const int end = g < w ? 31 : lane;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, j <= last ? fabsf(__uint_as_float(r[j])) : 0.0f);
+                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, j <= end ? fabsf(__uint_as_float(r[j])) : 0.0f);
                 }
-                const int e = lift_of(exponent_of(mx));
+                sm.row_top[group][row] = (uint8_t)exponent_of(mx);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.top_full);
+                if (!wait(&sm.top_full, i & 1)) break;
+                const int e = lift_of(max(sm.row_top[0][row], sm.row_top[1][row]));
                 lower = pow2(-e);
-                sm.row_lift[s][row] = (int8_t)e;
+                sm.row_lift[s][row] = (int8_t)e;  // (both groups write the same)
             }
             // (a product of the two factors on the diagonal is exact enough while the first,
             // which is above 1 there, and the second stay well inside float32)
             const bool steep = sm.g_hi[s][w * 32] - sm.g_hi[s][w * 32 + 31] > 100.0f;
-            uint32_t next[32];
-            tmem_ld32_start(sc, next);
 #pragma unroll 1
-            for (int g = 0; g <= w; ++g) {  // (the next block is loaded meanwhile)
+            for (int g = first; g < last; ++g) {
                 uint32_t r[32], out[16];
-                tmem_wait_for(next);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = next[j];
-                if (g < w) tmem_ld32_start(sc + (g + 1) * 32, next);
+                const int e = g * 32 + 31;
+                const float f = ex2_approx((hi - sm.g_hi[s][e]) + (lo - __half2float(sm.g_lo[s][e]))) * lower;
+                tmem_ld32(sc + g * 32, r);
                 if (g == w && steep) {
 #pragma unroll 1
                     for (int j = 0; j < 32; ++j) {
@@ -431,8 +491,6 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                         r[31] = __float_as_uint(x);
                     }
                 } else {
-                    const int e = g * 32 + 31;
-                    const float f = ex2_approx((hi - sm.g_hi[s][e]) + (lo - __half2float(sm.g_lo[s][e]))) * lower;
                     const u64 f2 = pk(f, f);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
@@ -452,12 +510,14 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                 }
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) out[j / 2] = HT::two(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-                tmem_st16(sc + g * 16, out);
+                tmem_st16(pw + g * 16, out);
             }
+            if (group) {
 #pragma unroll 1
-            for (int g = w + 1; g < 4; ++g) {  // behind it
-                const uint32_t none[16] = {};
-                tmem_st16(sc + g * 16, none);
+                for (int g = w + 1; g < 4; ++g) {  // behind the diagonal
+                    const uint32_t none[16] = {};
+                    tmem_st16(pw + g * 16, none);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
@@ -466,9 +526,11 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                 mbar_arrive(&sm.p_full);
                 mbar_arrive(&sm.g_empty[s]);
             }
+            if (group && !output(i, ex2_approx(hi) * p.scale)) break;
         }
     } else if (warp >= 8 && warp < 12) {
         // ------------------------------------------------------------- state --
+        more_registers<kRegsState>();
         const int w = warp & 3, row = w * 32 + lane;  // this thread's key
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
         unsigned char* const st = smem + kOffS;
@@ -477,7 +539,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         const int rows = (int)(p.P - p0 < DV ? p.P - p0 : DV);
         {
             // (unconditional loads of something valid, so that all are in flight at once)
-            const bool given = p.s_in && key && (a.pieces == 1 || (a.states_only && piece == 0));
+            const bool given = p.s_in && key && piece == 0;
             const float* at = given ? p.s_in + b * p.si_b + h * p.si_h + p0 * p.si_p + row * p.si_n : p.g;
             const int64_t step = given ? p.si_p : 0;
 #pragma unroll
@@ -488,25 +550,16 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 #pragma unroll
             for (int j = 0; j < DV; ++j) S[j] = given && j < rows ? S[j] : 0.0f;
         }
-        float* const rec = a.rec + unit * a.pieces * (DV * C) + row;  // S_0, then each piece's end
-        if (a.states_only) {
-            if (piece == 0) {
-                // S_0 goes through the workspace: the second launch's last piece may
-                // write state_out, in place, before another piece has begun
-#pragma unroll
-                for (int j = 0; j < DV; ++j) rec[j * C] = S[j];
-#pragma unroll
-                for (int j = 0; j < DV; ++j) S[j] = 0.0f;
-            }
-        } else if (a.pieces > 1) {  // through the pieces before this one
+        float* const rec = a.rec + unit * (a.pieces - 1) * (DV * C) + row;
+        if (a.phase == 2) {  // through the pieces before this one
             const float* end = rec;
             float f = 0.0f;
 #pragma unroll 1
-            for (int i = 0;; ++i) {
+            for (int i = 0;;) {
 #pragma unroll
                 for (int j = 0; j < DV; ++j) S[j] = fmaf(f, S[j], end[j * C]);
-                if (i == piece) break;
-                f = exp2f((float)a.rec_g[unit * a.pieces + i]);
+                if (++i == piece) break;
+                f = exp2f((float)a.rec_g[unit * (a.pieces - 1) + i]);
                 end += DV * C;
             }
         }
@@ -574,10 +627,10 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.kv_empty);
         }
-        if (start && a.states_only) {
+        if (start && a.phase == 1) {
 #pragma unroll
-            for (int j = 0; j < DV; ++j) rec[(piece + 1) * (DV * C) + j * C] = S[j];
-            if (row == 0) a.rec_g[unit * a.pieces + piece] = total;
+            for (int j = 0; j < DV; ++j) rec[piece * (DV * C) + j * C] = S[j];
+            if (row == 0) a.rec_g[unit * (a.pieces - 1) + piece] = total;
         } else if (start && p.s_out && piece == a.pieces - 1 && key) {
             float* at = p.s_out + b * p.so_b + h * p.so_h + p0 * p.so_p + row * p.so_n;
 #pragma unroll
@@ -586,57 +639,11 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                 at += p.so_p;
             }
         }
-    } else if (warp >= 12) {
-        // ---------------------------------------------------- V~ and output --
+    } else if (warp >= 12 && warp < 16) {
+        // ---------------------------------------------------------------- V~ --
+        fewer_registers<kRegs>();
         const int w = warp & 3, row = w * 32 + lane;  // this thread's token
-        const uint32_t lanes = (uint32_t)(w * 32) << 16;
         unsigned char* const vt = smem + kOffVt;
-        T* const out = static_cast<T*>(p.out) + b * p.o_b + h * p.o_h + p0;
-        float across = 0.0f, across_next = 0.0f;  // scale exp(G_t)
-        auto output = [&](int i) {
-            if (!wait(&sm.o_full, i & 1)) return false;
-            tc_fence_after();
-            float inside = p.scale, over = across;
-            if (HT::kScaled) {
-                over *= pow2(sm.s_lift[i & 1]);
-                inside *= pow2(sm.row_lift[i & 1][row]);
-            }
-            const int64_t t = (c0 + i) * C + row;
-            T* const orow = out + t * p.o_t;
-            const u64 over2 = pk(over, over), inside2 = pk(inside, inside);
-#pragma unroll 1
-            for (int g = 0; g < DV; g += 32) {
-                uint32_t x[32], y[32], o[16];
-                tmem_ld32x2(tm + lanes + kOa + g, tm + lanes + kOb + g, x, y);
-                if (g == DV - 32) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.o_empty);
-                }
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    float f0, f1;
-                    upk(ffma2(pk(__uint_as_float(y[j]), __uint_as_float(y[j + 1])), over2,
-                              fmul2(pk(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), inside2)), f0, f1);
-                    o[j / 2] = HT::two(f0, f1);
-                }
-                if (t < len) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 16) {
-                        if (p0 + g + j >= p.P) break;
-                        if (a.out32) {  // a whole 32-byte sector
-                            store32(orow + g + j, o + j / 2);
-                        } else {
-                            const uint32_t* v = o + j / 2;
-                            *reinterpret_cast<uint4*>(orow + g + j) = make_uint4(v[0], v[1], v[2], v[3]);
-                            if (p0 + g + j + 8 < p.P)
-                                *reinterpret_cast<uint4*>(orow + g + j + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-                        }
-                    }
-                }
-            }
-            return true;
-        };
         auto values = [&](int i) {
             const int s = i & 1;
             const uint32_t ph = (i >> 1) & 1;
@@ -644,7 +651,6 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             unsigned char* const vrow = v_tile(s) + row * 128;
             const float hi = sm.g_hi[s][row], lo = __half2float(sm.g_lo[s][row]);
             const float weight = ex2_approx((sm.g_hi[s][C - 1] - hi) + (__half2float(sm.g_lo[s][C - 1]) - lo));
-            across_next = ex2_approx(hi) * p.scale;
             if ((c0 + i) * C + row >= len) {  // rows behind the end may hold anything
                 const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
@@ -689,15 +695,13 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sm.vt_full);
+                mbar_arrive(&sm.empty_v[s]);
                 mbar_arrive(&sm.g_empty[s]);
             }
             return true;
         };
-        for (int i = -1; start && i < n; ++i) {
-            across = across_next;
-            if (i + 1 < n && !values(i + 1)) break;
-            if (outputs && i >= 0 && !output(i)) break;
-        }
+        for (int i = 0; start && i < n; ++i)
+            if (!values(i)) break;
     }
     __syncthreads();
     tc_fence_after();
@@ -759,8 +763,8 @@ int linattn_chunk_tokens() { return C; }
 int linattn_chunk_values() { return DV; }
 uint64_t linattn_chunk_record_bytes() { return DV * C * 4; }
 
-cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, int pieces, int64_t per_piece, float* rec,
-                                 double* rec_g, long long wait_budget, int dev, cudaStream_t s) {
+cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, const LinAttnPieces& cut, float* rec, double* rec_g,
+                                 long long wait_budget, int dev, cudaStream_t s) {
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, p.io_dt, p.q, p.N, p.L, p.Hk, p.Bn, p.q_t, p.q_h, p.q_b) ||
         !make_map(&mk, p.io_dt, p.k, p.N, p.L, p.Hk, p.Bn, p.k_t, p.k_h, p.k_b) ||
@@ -769,9 +773,9 @@ cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, int pie
     ChunkArgs a{};
     a.p = p;
     a.pt = (p.P + DV - 1) / DV;
-    a.chunks = (p.L + C - 1) / C;
-    a.pieces = pieces;
-    a.per_piece = per_piece;
+    a.pieces = cut.pieces;
+    a.piece0 = cut.piece0;
+    a.per_piece = cut.per_piece;
     a.rec = rec;
     a.rec_g = rec_g;
     a.out32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.P % 16 == 0 && p.o_b % 16 == 0 && p.o_h % 16 == 0 &&
@@ -779,16 +783,15 @@ cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, int pie
     a.err = device_error_ptr(dev);
     if (!a.err) return cudaErrorUnknown;
     a.wait_budget = wait_budget;
-    cudaError_t e = cudaSuccess;
-    if (pieces > 1) {
-        a.states_only = 1;
-        e = p.io_dt == kF16 ? launch_t<__half>(mq, mk, mv, a, units * (pieces - 1), s)
-                            : launch_t<__nv_bfloat16>(mq, mk, mv, a, units * (pieces - 1), s);
+    const bool f16 = p.io_dt == kF16;
+    const int64_t grid = cut.pieces > 1 ? units * (cut.pieces - 1) : units;
+    if (cut.pieces > 1) {
+        a.phase = 1;
+        const cudaError_t e = f16 ? launch_t<__half>(mq, mk, mv, a, grid, s) : launch_t<__nv_bfloat16>(mq, mk, mv, a, grid, s);
         if (e != cudaSuccess) return e;
-        a.states_only = 0;
+        a.phase = 2;
     }
-    return p.io_dt == kF16 ? launch_t<__half>(mq, mk, mv, a, units * pieces, s)
-                           : launch_t<__nv_bfloat16>(mq, mk, mv, a, units * pieces, s);
+    return f16 ? launch_t<__half>(mq, mk, mv, a, grid, s) : launch_t<__nv_bfloat16>(mq, mk, mv, a, grid, s);
 }
 
 }  // namespace ssm

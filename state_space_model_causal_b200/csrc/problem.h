@@ -342,9 +342,13 @@ int linattn_chunk_smem();
 int linattn_chunk_tokens();               // tokens per chunk
 int linattn_chunk_values();               // values per CTA
 uint64_t linattn_chunk_record_bytes();    // one state of a CTA
-// pieces > 1: rec holds units * pieces records, rec_g as many doubles
-cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, int pieces, int64_t per_piece, float* rec,
-                                 double* rec_g, long long wait_budget, int dev, cudaStream_t s);
+struct LinAttnPieces {
+    int pieces;                 // pieces per sequence
+    int64_t piece0, per_piece;  // chunks of the first, and of each other
+};
+// pieces > 1: rec holds units * (pieces - 1) records, rec_g as many doubles
+cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, const LinAttnPieces& cut, float* rec, double* rec_g,
+                                 long long wait_budget, int dev, cudaStream_t s);
 cudaError_t launch_linattn_step(const LinAttnStepProblem& p, int kernel, int grid, cudaStream_t s);
 int linattn_step_bulk_rows(int st_dt, int64_t N);  // rows of the state per item of the bulk-copy kernel
 cudaError_t launch_linattn_step_bulk(const LinAttnStepProblem& p, int sms, int dev, long long wait_budget, cudaStream_t s);

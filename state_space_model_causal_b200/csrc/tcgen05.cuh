@@ -146,21 +146,21 @@ __device__ __forceinline__ constexpr uint32_t mma_desc(uint32_t type, bool trans
 #define SSM_MMA8_STEP(A)                                                            \
     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], " A ", b, %3, 1;\n\t"
 template <int A_STEP, int A_JUMP, int B_STEP, int B_JUMP>
-__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool on = true) {
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc) {
     asm volatile(
         "{\n\t.reg .pred e, z;\n\t.reg .b64 a, b;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.and.u32 e, %4, 0, e;\n\tsetp.ne.u32 z, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 z, 0, 0;\n\t"
         "mov.b64 a, %1;\n\tmov.b64 b, %2;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, z;\n\t"
+        "add.u64 a, a, %4;\n\tadd.u64 b, b, %6;\n\t" SSM_MMA8_STEP("a")
+        "add.u64 a, a, %4;\n\tadd.u64 b, b, %6;\n\t" SSM_MMA8_STEP("a")
+        "add.u64 a, a, %4;\n\tadd.u64 b, b, %6;\n\t" SSM_MMA8_STEP("a")
         "add.u64 a, a, %5;\n\tadd.u64 b, b, %7;\n\t" SSM_MMA8_STEP("a")
-        "add.u64 a, a, %5;\n\tadd.u64 b, b, %7;\n\t" SSM_MMA8_STEP("a")
-        "add.u64 a, a, %5;\n\tadd.u64 b, b, %7;\n\t" SSM_MMA8_STEP("a")
-        "add.u64 a, a, %6;\n\tadd.u64 b, b, %8;\n\t" SSM_MMA8_STEP("a")
-        "add.u64 a, a, %5;\n\tadd.u64 b, b, %7;\n\t" SSM_MMA8_STEP("a")
-        "add.u64 a, a, %5;\n\tadd.u64 b, b, %7;\n\t" SSM_MMA8_STEP("a")
-        "add.u64 a, a, %5;\n\tadd.u64 b, b, %7;\n\t" SSM_MMA8_STEP("a")
+        "add.u64 a, a, %4;\n\tadd.u64 b, b, %6;\n\t" SSM_MMA8_STEP("a")
+        "add.u64 a, a, %4;\n\tadd.u64 b, b, %6;\n\t" SSM_MMA8_STEP("a")
+        "add.u64 a, a, %4;\n\tadd.u64 b, b, %6;\n\t" SSM_MMA8_STEP("a")
         "}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"(on ? 1u : 0u), "n"(A_STEP), "n"(A_JUMP), "n"(B_STEP), "n"(B_JUMP)
+        "l"(a), "l"(b), "r"(desc), "n"(A_STEP), "n"(A_JUMP), "n"(B_STEP), "n"(B_JUMP)
         : "memory");
 }
 #undef SSM_MMA8_STEP

@@ -183,13 +183,26 @@ def test_prompt_then_tokens_equals_one_prompt(io):
     assert (np.abs(to_np(S) - Sr) <= bs).all()
 
 
-def test_a_long_sequence_in_pieces_or_whole():
-    """Few long sequences are cut into pieces where a workspace is given; with
-    and without it the results agree with the definition."""
-    args = problem(1, 2, 2, 3000, 64, 64, "bf16", "token", seed=8)
+@pytest.mark.parametrize("io", ["bf16", "f16"])
+@pytest.mark.parametrize("L,lens", [(3000, None), (1600, [1600, 0, 130, 900]), (2048, [2048, 2047, 128, 1])])
+def test_long_sequences_in_pieces_or_whole(io, L, lens):
+    """Few long sequences are cut into pieces where a workspace is given (ends
+    of sequences before, in and between pieces); with and without it the
+    results agree with the definition, the state updated in place too."""
+    import torch
+    from state_space_model_causal_b200 import ssm_linear_attention_fwd
+    B = 1 if lens is None else len(lens)
+    args = problem(B, 2, 1, L, 64, 64, io, "token", seed=8)
     for ws in ("auto", None):
-        out, S, kern = run(*args, io="bf16", workspace=ws)
-        check(args, 1.0, None, "bf16", out, S, kern)
+        out, S, kern = run(*args, lens=lens, io=io, workspace=ws)
+        assert kern == "linattn_chunk"
+        check(args, 1.0, lens, io, out, S, kern)
+    q, k, v, g, s0 = args
+    st = T(s0, "f32")
+    li = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ssm_linear_attention_fwd(token_major(q, io), token_major(k, io), token_major(v, io), T(g, "f32"), state=st, seq_lens=li)
+    out, S, _ = run(*args, lens=lens, io=io)
+    np.testing.assert_array_equal(to_np(st), S)
 
 
 # -------------------------------------------------------------- one token --
