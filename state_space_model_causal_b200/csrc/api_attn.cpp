@@ -336,6 +336,9 @@ ssm_status paged_impl(const ssm_paged_attention_args* a, cudaStream_t stream, ui
 
     PagedProblem p{};
     p.Bn = B; p.Hq = Hq; p.Hkv = Hkv; p.D = D; p.page = (int)page; p.pages = pages; p.M = M;
+    p.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (page == (int64_t)1 << i) p.page_shift = i;
     p.G = Hq / Hkv; p.cap = cap; p.io_dt = io;
     p.hpb = paged_heads_per_cta(kernel, p.G);
     p.hblocks = (int)((p.G + p.hpb - 1) / p.hpb);

@@ -381,7 +381,9 @@ __device__ __forceinline__ uint32_t word(const uint4& u, int i) {
     return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
 }
 
-template <typename T, int DP, bool WIDE>
+// WHOLE: pages of a multiple of 16 tokens, so that a block of 16 lies in one page and has one
+// address; else every token's row is looked up by a lane and handed round.
+template <typename T, int DP, bool WIDE, bool WHOLE>
 __global__ void __launch_bounds__(kBlock, WIDE ? 2 : 3) paged_mma_kernel(const PagedProblem p) {
     constexpr int HPB = WIDE ? 16 : 8, KI = DP / 32, VI = DP / 64;
     constexpr int NB = DP == 64 && !WIDE ? 2 : 1;  // blocks of 16 tokens loaded together: 128 registers' worth
@@ -414,42 +416,65 @@ __global__ void __launch_bounds__(kBlock, WIDE ? 2 : 3) paged_mma_kernel(const P
             m[w] = kNegInf;
             l[w] = 0.0f;
         }
-        // lane i looks after token t + i: its page, one step ahead
-        auto page_of = [&](int t) {
-            const int tok = t + (lane & (16 * NB - 1));
-            return tok < t1 ? table[(int64_t)((uint32_t)tok / (uint32_t)p.page) * p.tb_m] : -1;
+        auto page_index = [&](int tok) {
+            return p.page_shift >= 0 ? tok >> p.page_shift : (int)((uint32_t)tok / (uint32_t)p.page);
         };
-        int32_t pg = page_of(t0 + warp * 16 * NB);
+        // the pages of a step, looked up one step ahead: WHOLE: pg[nb] is block nb's;
+        // else pg[0] is that of token t + lane
+        auto look_up = [&](int t, int32_t (&pg)[NB]) {
+#pragma unroll
+            for (int nb = 0; nb < (WHOLE ? NB : 1); ++nb) {
+                const int tok = WHOLE ? t + 16 * nb : t + (lane & (16 * NB - 1));
+                pg[nb] = tok < t1 ? table[(int64_t)page_index(tok) * p.tb_m] : -1;
+            }
+        };
+        int32_t pg[NB];
+        look_up(t0 + warp * 16 * NB, pg);
         for (int t2 = t0 + warp * 16 * NB; t2 < t1; t2 += 16 * NB * kWarps) {
-            const int tok = t2 + (lane & (16 * NB - 1));
-            const bool there = pg >= 0 && pg < p.pages;
-            const int64_t row = (uint32_t)tok % (uint32_t)p.page;
-            const int64_t ko = there ? pg * p.k_g + row * p.k_t : -1, vo = there ? pg * p.v_g + row * p.v_t : -1;
             uint4 kf[NB][2][KI], vf[NB][4][VI];
             bool on_all[NB][4];
+            int64_t ko = -1, vo = -1;
+            if (!WHOLE) {
+                const int tok = t2 + (lane & (16 * NB - 1));
+                const int64_t row = tok - page_index(tok) * p.page;
+                if (pg[0] >= 0 && pg[0] < p.pages) {
+                    ko = pg[0] * p.k_g + row * p.k_t;
+                    vo = pg[0] * p.v_g + row * p.v_t;
+                }
+            }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
+                int valid = 0;  // WHOLE: tokens of the block that are there
+                const T *kb = kh, *vb = vh;
+                if (WHOLE) {
+                    const int t = t2 + 16 * nb;
+                    const int64_t row = t - page_index(t) * p.page;
+                    if (pg[nb] >= 0 && pg[nb] < p.pages) {
+                        valid = t1 - t;
+                        kb = kh + pg[nb] * p.k_g + (row + r) * p.k_t + 8 * c;
+                        vb = vh + pg[nb] * p.v_g + (row + 2 * c) * p.v_t + 8 * r;
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int64_t at = shfl64(ko, 16 * nb + r + 8 * j);
+                    const int64_t at = WHOLE ? 0 : shfl64(ko, 16 * nb + r + 8 * j);
+                    const T* const row = WHOLE ? kb + 8 * j * p.k_t : kh + at + 8 * c;
+                    const bool on = WHOLE ? r + 8 * j < valid : at >= 0;
 #pragma unroll
-                    for (int i = 0; i < KI; ++i) {
-                        const int d = 32 * i + 8 * c;
-                        kf[nb][j][i] = at >= 0 && d < p.D ? ld_stream16(kh + at + d) : zero;
-                    }
+                    for (int i = 0; i < KI; ++i) kf[nb][j][i] = on && 32 * i + 8 * c < p.D ? ld_stream16(row + 32 * i) : zero;
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int64_t at = shfl64(vo, 16 * nb + 2 * c + (j & 1) + 8 * (j >> 1));
-                    on_all[nb][j] = at >= 0;
+                    const int q = (j & 1) + 8 * (j >> 1);  // this lane's token 2 c + q
+                    const int64_t at = WHOLE ? 0 : shfl64(vo, 16 * nb + 2 * c + q);
+                    const T* const row = WHOLE ? vb + q * p.v_t : vh + at + 8 * r;
+                    const bool on = WHOLE ? 2 * c + q < valid : at >= 0;
+                    on_all[nb][j] = on;
 #pragma unroll
-                    for (int i = 0; i < VI; ++i) {
-                        const int d = 64 * i + 8 * r;
-                        vf[nb][j][i] = at >= 0 && d < p.D ? ld_stream16(vh + at + d) : zero;
-                    }
+                    for (int i = 0; i < VI; ++i) vf[nb][j][i] = on && 64 * i + 8 * r < p.D ? ld_stream16(row + 64 * i) : zero;
                 }
             }
-            pg = page_of(t2 + 16 * NB * kWarps);
+            look_up(t2 + 16 * NB * kWarps, pg);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const int t = t2 + 16 * nb;
@@ -690,14 +715,14 @@ cudaError_t launch_after(void (*fn)(const PagedProblem), unsigned grid, const Pa
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
-template <typename T>
+template <typename T, bool WHOLE>
 void mma_t(const PagedProblem& p, dim3 grid, cudaStream_t s) {
     if (p.hpb == 16) {
-        if (p.D <= 64) paged_mma_kernel<T, 64, true><<<grid, kBlock, 0, s>>>(p);
-        else paged_mma_kernel<T, 128, true><<<grid, kBlock, 0, s>>>(p);
+        if (p.D <= 64) paged_mma_kernel<T, 64, true, WHOLE><<<grid, kBlock, 0, s>>>(p);
+        else paged_mma_kernel<T, 128, true, WHOLE><<<grid, kBlock, 0, s>>>(p);
     } else {
-        if (p.D <= 64) paged_mma_kernel<T, 64, false><<<grid, kBlock, 0, s>>>(p);
-        else paged_mma_kernel<T, 128, false><<<grid, kBlock, 0, s>>>(p);
+        if (p.D <= 64) paged_mma_kernel<T, 64, false, WHOLE><<<grid, kBlock, 0, s>>>(p);
+        else paged_mma_kernel<T, 128, false, WHOLE><<<grid, kBlock, 0, s>>>(p);
     }
 }
 
@@ -724,8 +749,9 @@ int paged_ctas_per_sm(int kernel, int64_t G, int64_t D) {
 cudaError_t launch_paged(const PagedProblem& p, int kernel, cudaStream_t s) {
     const dim3 grid((unsigned)p.workers, (unsigned)(p.Hkv * p.hblocks));
     if (kernel == SSM_KERNEL_PAGED_DECODE) {
-        if (p.io_dt == kF16) mma_t<__half>(p, grid, s);
-        else mma_t<__nv_bfloat16>(p, grid, s);
+        const bool whole = p.page % 16 == 0;
+        if (p.io_dt == kF16) whole ? mma_t<__half, true>(p, grid, s) : mma_t<__half, false>(p, grid, s);
+        else whole ? mma_t<__nv_bfloat16, true>(p, grid, s) : mma_t<__nv_bfloat16, false>(p, grid, s);
     } else if (p.io_dt == kF16) generic_t<__half>(p, grid, s);
     else if (p.io_dt == kBF16) generic_t<__nv_bfloat16>(p, grid, s);
     else generic_t<float>(p, grid, s);

@@ -258,6 +258,7 @@ struct LinAttnStepProblem {
 struct PagedProblem {
     int64_t Bn, Hq, Hkv, D, pages, M;
     int page;             // rows per page
+    int page_shift;       // its logarithm, or -1
     int64_t G;            // Hq / Hkv
     int64_t cap;          // M * page: the longest length, < 2^31
     int hpb;              // query heads per CTA
