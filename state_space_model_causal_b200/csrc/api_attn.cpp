@@ -182,12 +182,12 @@ ssm_status linattn_impl(const ssm_linattn_args* a, cudaStream_t stream, uint64_t
                                     reinterpret_cast<double*>(ws + rec), kWaitBudget, dev, stream) == cudaSuccess
                    ? SSM_OK : SSM_ERR_CUDA;
     }
-    const int64_t rows = linattn_generic_rows(), blocks = (P + rows - 1) / rows;
+    const int64_t rows = linattn_generic_rows(B * H, P, sm_count(dry)), blocks = (P + rows - 1) / rows;
     if (B * H > INT32_MAX / blocks) return SSM_ERR_UNSUPPORTED;
     const int grid = (int)(B * H * blocks);
     fill_info(a->info, SSM_KERNEL_LINATTN_GENERIC, grid, linattn_generic_block(), 0, rows, B * H * blocks);
     if (dry || ws_query) return SSM_OK;
-    return launch_linattn_generic(p, grid, stream) == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+    return launch_linattn_generic(p, (int)rows, grid, stream) == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
 // ----------------------------------------------- linear attention, one token --

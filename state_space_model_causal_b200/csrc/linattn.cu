@@ -8,8 +8,8 @@
 // products and its sums are float32 throughout.
 //
 //   linattn_generic_kernel  a prompt of any strides, types and sizes (N <= 256):
-//                           a warp carries 4 rows of S in registers over the
-//                           whole sequence.
+//                           a warp carries 4 rows of S (2 where there are few) in
+//                           registers over the whole sequence.
 //   linattn_step_bulk_kernel one token: S is read and written once, by bulk copies
 //                           through shared memory (rows without gaps).
 //   linattn_step_kernel     one token, rows of 16-byte vectors with gaps.
@@ -25,7 +25,6 @@ namespace ssm {
 namespace {
 
 constexpr int kBlock = 128;   // 4 warps
-constexpr int kWarpRows = 4;  // rows of S per warp of the generic prompt kernel
 
 // a positive log decay counts as 0 (a NaN stays one)
 __device__ __forceinline__ float decay_log(float g) { return g > 0.0f ? 0.0f : g; }
@@ -60,7 +59,7 @@ __device__ __forceinline__ float reduce_many(float (&v)[K], int lane) {
 // Prompt, any layout.  Bound by the latency of a token's chain (decay and FMA,
 // then the reduction, whose result nothing waits for): U tokens are loaded
 // while the U before them are computed, and their 4 U sums reduced together.
-template <typename T, int NE, int U>
+template <typename T, int NE, int U, int kWarpRows>
 __global__ void __launch_bounds__(kBlock) linattn_generic_kernel(const LinAttnProblem p) {
     const int lane = threadIdx.x & 31;
     const int64_t nblk = (p.P + 4 * kWarpRows - 1) / (4 * kWarpRows);
@@ -88,13 +87,13 @@ __global__ void __launch_bounds__(kBlock) linattn_generic_kernel(const LinAttnPr
     const float* g = p.g + b * p.g_b + h * p.g_h;
     T* out = static_cast<T*>(p.out) + b * p.o_b + h * p.o_h;
 
-    float kn[U][NE], qn[U][NE], vn[U][kWarpRows], gn[U];
+    float kn[U][NE], qn[U][NE], vn[U][kWarpRows], gn = 0.0f;  // gn: of token lane % U
     auto load = [&](int64_t t0) {
+        gn = t0 + lane % U < len ? decay_log(g[(t0 + lane % U) * p.g_t]) : 0.0f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t t = t0 + u;
             const bool on = t < len;
-            gn[u] = on ? decay_log(g[t * p.g_t]) : 0.0f;
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
                 const int64_t n = lane + 32 * i;
@@ -113,10 +112,13 @@ __global__ void __launch_bounds__(kBlock) linattn_generic_kernel(const LinAttnPr
         // of its distance from 1 does not.
         float kc[U][NE], qc[U][NE], vc[U][kWarpRows], lam[U];
         bool near1[U];
+        const bool near = gn > -0.6931f;
+        const float decay = near ? expm1f(gn) : expf(gn);
+        const uint32_t nears = __ballot_sync(0xffffffffu, near);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            near1[u] = gn[u] > -0.6931f;
-            lam[u] = near1[u] ? expm1f(gn[u]) : expf(gn[u]);
+            near1[u] = nears >> u & 1;
+            lam[u] = __shfl_sync(0xffffffffu, decay, u);
 #pragma unroll
             for (int i = 0; i < NE; ++i) kc[u][i] = kn[u][i], qc[u][i] = qn[u][i];
 #pragma unroll
@@ -156,12 +158,12 @@ __global__ void __launch_bounds__(kBlock) linattn_generic_kernel(const LinAttnPr
         }
 }
 
-template <typename T>
+template <typename T, int R>
 cudaError_t generic_t(const LinAttnProblem& p, int grid, cudaStream_t s) {
-    if (p.N <= 32) linattn_generic_kernel<T, 1, 4><<<grid, kBlock, 0, s>>>(p);
-    else if (p.N <= 64) linattn_generic_kernel<T, 2, 4><<<grid, kBlock, 0, s>>>(p);
-    else if (p.N <= 128) linattn_generic_kernel<T, 4, 4><<<grid, kBlock, 0, s>>>(p);
-    else linattn_generic_kernel<T, 8, 2><<<grid, kBlock, 0, s>>>(p);
+    if (p.N <= 32) linattn_generic_kernel<T, 1, 4, R><<<grid, kBlock, 0, s>>>(p);
+    else if (p.N <= 64) linattn_generic_kernel<T, 2, 4, R><<<grid, kBlock, 0, s>>>(p);
+    else if (p.N <= 128) linattn_generic_kernel<T, 4, 4, R><<<grid, kBlock, 0, s>>>(p);
+    else linattn_generic_kernel<T, 8, 2, R><<<grid, kBlock, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -500,12 +502,21 @@ cudaError_t bulk_t(const LinAttnStepProblem& p, int sms, int rows, DeviceError* 
 }  // namespace
 
 int linattn_generic_block() { return kBlock; }
-int linattn_generic_rows() { return (kBlock / 32) * kWarpRows; }
+int linattn_generic_rows(int64_t heads, int64_t P, int sms) {
+    // rows per CTA: 4 per warp, 2 while that leaves less than 3 CTAs per SM (the kernel waits for a
+    // token's chain: more warps hide it, more rows per warp share its loads)
+    return heads * ((P + 15) / 16) >= (int64_t)3 * sms ? 16 : 8;
+}
 
-cudaError_t launch_linattn_generic(const LinAttnProblem& p, int grid, cudaStream_t s) {
-    if (p.io_dt == kF16) return generic_t<__half>(p, grid, s);
-    if (p.io_dt == kBF16) return generic_t<__nv_bfloat16>(p, grid, s);
-    return generic_t<float>(p, grid, s);
+cudaError_t launch_linattn_generic(const LinAttnProblem& p, int rows, int grid, cudaStream_t s) {
+    if (rows == 8) {
+        if (p.io_dt == kF16) return generic_t<__half, 2>(p, grid, s);
+        if (p.io_dt == kBF16) return generic_t<__nv_bfloat16, 2>(p, grid, s);
+        return generic_t<float, 2>(p, grid, s);
+    }
+    if (p.io_dt == kF16) return generic_t<__half, 4>(p, grid, s);
+    if (p.io_dt == kBF16) return generic_t<__nv_bfloat16, 4>(p, grid, s);
+    return generic_t<float, 4>(p, grid, s);
 }
 
 int linattn_step_block() { return kBlock; }

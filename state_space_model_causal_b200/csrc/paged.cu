@@ -386,7 +386,7 @@ __device__ __forceinline__ uint32_t word(const uint4& u, int i) {
 template <typename T, int DP, bool WIDE, bool WHOLE>
 __global__ void __launch_bounds__(kBlock, WIDE ? 2 : 3) paged_mma_kernel(const PagedProblem p) {
     constexpr int HPB = WIDE ? 16 : 8, KI = DP / 32, VI = DP / 64;
-    constexpr int NB = DP == 64 && !WIDE ? 2 : 1;  // blocks of 16 tokens loaded together: 128 registers' worth
+    constexpr int NB = DP == 64 ? 2 : 1;  // blocks of 16 tokens loaded together
     constexpr int ROWS = WIDE ? 2 : 1;  // query rows per lane
     using M = Pack<T>;
     __shared__ Join<HPB, DP> sm;

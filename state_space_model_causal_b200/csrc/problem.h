@@ -335,9 +335,9 @@ cudaError_t launch_gated_conv(const GatedConvProblem& p, int kernel, int grid, i
 int gated_conv_ring_smem_bytes();  // dynamic shared memory of the vector kernel's CTA
 int gated_conv_ctas_per_sm();      // CTAs of the vector kernel resident per SM
 int gated_conv_block();            // threads per CTA of both kernels
-cudaError_t launch_linattn_generic(const LinAttnProblem& p, int grid, cudaStream_t s);
+cudaError_t launch_linattn_generic(const LinAttnProblem& p, int rows, int grid, cudaStream_t s);
 int linattn_generic_block();
-int linattn_generic_rows();  // rows of the state per CTA
+int linattn_generic_rows(int64_t heads, int64_t P, int sms);  // rows of the state per CTA
 int linattn_chunk_block();
 int linattn_chunk_smem();
 int linattn_chunk_tokens();               // tokens per chunk
