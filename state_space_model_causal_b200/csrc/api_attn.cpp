@@ -174,7 +174,7 @@ ssm_status linattn_impl(const ssm_linattn_args* a, cudaStream_t stream, uint64_t
                 if (present(*t) && overlap(ws, *t)) return SSM_ERR_ALIAS;
         }
         if (units > INT32_MAX / pieces) return SSM_ERR_UNSUPPORTED;
-        fill_info(a->info, SSM_KERNEL_LINATTN_CHUNK, (int)(units * std::max<int64_t>(pieces - 1, 1)), linattn_chunk_block(), linattn_chunk_smem(),
+        fill_info(a->info, SSM_KERNEL_LINATTN_CHUNK, (int)(units * std::max<int64_t>(pieces - 1, 1)), linattn_chunk_block(), linattn_chunk_smem(io),
                   linattn_chunk_values(), units * pieces);
         if (dry) return SSM_OK;
         char* ws = static_cast<char*>(a->workspace);

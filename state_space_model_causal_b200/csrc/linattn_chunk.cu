@@ -30,8 +30,8 @@
 //   16-19  the scores' other blocks, then the output
 //
 // Precision.  Accumulators and S are float32.  V~ is given to the tensor cores as
-// two 16-bit numbers, the second holding what rounding the first left over (16
-// bits of significand for bf16, 22 for f16), because the state is a float32 result and
+// several 16-bit numbers, each holding what rounding those before it left over (three
+// for bf16: 24 bits of significand, two for f16: 22), because the state is a float32 result and
 // remembers for long.  The scores, and the copy of S that Q S reads, are
 // rounded once, as the output will be.  For f16, whose range is small, a power of two is taken out of every row of
 // scores, of V~ and of S, and put back in float32: it costs three maxima.
@@ -55,10 +55,34 @@ constexpr int C = 128;        // tokens per chunk
 constexpr int DV = 64;        // values per CTA
 constexpr int kBlockBytes = C * 128;               // a tile: 128 rows of 64 16-bit elements
 constexpr int kStageBytes = 5 * kBlockBytes;       // Q (2 tiles), K (2), V (1)
-constexpr int kOffVt = 2 * kStageBytes;            // V~ high, low
-constexpr int kOffS = kOffVt + 2 * kBlockBytes;    // S
-constexpr int kTiles = kOffS + kBlockBytes;        // 212,992 bytes
+constexpr int kOffS = 2 * kStageBytes;             // S
+constexpr int kOffVt = kOffS + kBlockBytes;        // V~: Half16<T>::kParts tiles
 
+template <typename T> struct Half16;
+template <> struct Half16<__half> {
+    static constexpr uint32_t kType = 0;
+    static constexpr bool kScaled = true;
+    static constexpr int kParts = 2;  // numbers that hold a value of V~
+    __device__ __forceinline__ static uint32_t two(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ __forceinline__ static float2 back(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+};
+template <> struct Half16<__nv_bfloat16> {
+    static constexpr uint32_t kType = 1;
+    static constexpr bool kScaled = false;
+    static constexpr int kParts = 3;
+    __device__ __forceinline__ static uint32_t two(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __device__ __forceinline__ static float2 back(uint32_t u) {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+    }
+};
+
+template <typename T>
 struct Small {
     uint64_t full_qk[2], full_v[2], empty_qk[2], empty_v[2];  // loads
     uint64_t g_full[2], g_empty[2];                           // decay sums
@@ -68,17 +92,22 @@ struct Small {
     int abort;
     uint8_t red[2][2][4];      // f16: exponents of the largest values, per warp
     int s_lift[2], v_lift[2];  // f16: S, V~ were divided by 2^lift
-    int8_t row_lift[2][C];     // f16: so was a row of scores
-    uint8_t row_top[2][C];     // f16: exponent of a row's largest score, of either group
+    static constexpr int kRows = Half16<T>::kScaled ? C : 1;
+    int8_t row_lift[2][kRows]; // f16: so was a row of scores
+    uint8_t row_top[2][kRows]; // f16: exponent of a row's largest score, of either group
     alignas(16) float g_hi[2][C], column[2][C];  // read as vectors
     __half g_lo[2][C];         // remainder of g_hi, below 2^-24 of it
 };
-constexpr int kSmem = kTiles + sizeof(Small);
-static_assert(kSmem <= 232448, "shared memory of one CTA");
-static_assert(kTiles % 16 == 0, "alignment of the vectors behind the tiles");
+template <typename T>
+struct Layout {
+    static constexpr int kTiles = kOffVt + Half16<T>::kParts * kBlockBytes, kSmem = kTiles + (int)sizeof(Small<T>);
+    static_assert(kSmem <= 232448, "shared memory of one CTA");
+    static_assert(kTiles % 16 == 0, "alignment of the vectors behind the tiles");
+};
 
 // tensor memory columns
 constexpr uint32_t kSc = 0, kP = 128, kOa = 192, kOb = 256, kKv = 320, kColumns = 512;
+static_assert(kKv + Half16<__nv_bfloat16>::kParts * DV <= kColumns, "tensor memory of one CTA");
 
 struct ChunkArgs {
     LinAttnProblem p;
@@ -106,8 +135,9 @@ __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* a
         }
     }
 }
+template <typename T>
 struct Waiter {
-    Small* sm;
+    Small<T>* sm;
     const ChunkArgs* a;
     // by one thread
     __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
@@ -119,28 +149,6 @@ struct Waiter {
     }
 };
 
-template <typename T> struct Half16;
-template <> struct Half16<__half> {
-    static constexpr uint32_t kType = 0;
-    static constexpr bool kScaled = true;
-    __device__ __forceinline__ static uint32_t two(float a, float b) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    __device__ __forceinline__ static float2 back(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
-};
-template <> struct Half16<__nv_bfloat16> {
-    static constexpr uint32_t kType = 1;
-    static constexpr bool kScaled = false;
-    __device__ __forceinline__ static uint32_t two(float a, float b) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    __device__ __forceinline__ static float2 back(uint32_t u) {
-        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
-    }
-};
-
 // e with top * 2^-e in [2^13, 2^14), from the exponent field of top >= 0 (0 if top is 0 or not
 // finite); limited so that 2^e and 2^-e are normal numbers.
 __device__ __forceinline__ int lift_of(uint32_t exponent) {
@@ -149,15 +157,17 @@ __device__ __forceinline__ int lift_of(uint32_t exponent) {
 __device__ __forceinline__ uint32_t exponent_of(float v) { return __float_as_uint(v) >> 23 & 255u; }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// two 16-bit numbers per value: f = hi + lo, for a pair
+// 16-bit numbers that add up to a value, for a pair
 template <typename T>
-__device__ __forceinline__ void split2(u64 f, uint32_t& hi, uint32_t& lo) {
-    float x, y;
-    upk(f, x, y);
-    hi = Half16<T>::two(x, y);
-    const float2 back = Half16<T>::back(hi);
-    upk(fsub2(f, pk(back.x, back.y)), x, y);
-    lo = Half16<T>::two(x, y);
+__device__ __forceinline__ void split2(u64 f, uint32_t (&part)[Half16<T>::kParts]) {
+#pragma unroll
+    for (int i = 0; i < Half16<T>::kParts; ++i) {
+        float x, y;
+        upk(f, x, y);
+        part[i] = Half16<T>::two(x, y);
+        const float2 back = Half16<T>::back(part[i]);
+        f = fsub2(f, pk(back.x, back.y));
+    }
 }
 
 __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
@@ -189,7 +199,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ ChunkArgs a) {
     using HT = Half16<T>;
     extern __shared__ __align__(1024) unsigned char smem[];
-    Small& sm = *reinterpret_cast<Small*>(smem + kTiles);
+    Small<T>& sm = *reinterpret_cast<Small<T>*>(smem + Layout<T>::kTiles);
     const LinAttnProblem& p = a.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int n_pieces = a.phase == 0 ? 1 : a.pieces - 1;
@@ -244,7 +254,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = __shfl_sync(0xffffffffu, sm.tmem, 0);
-    const Waiter wait{&sm, &a};
+    const Waiter<T> wait{&sm, &a};
     const bool start = sm.abort == 0;
     auto q_tile = [&](int s) { return smem + s * kStageBytes; };
     auto k_tile = [&](int s) { return smem + s * kStageBytes + 2 * kBlockBytes; };
@@ -304,7 +314,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         // steps after it was last read.
         constexpr uint32_t d_qk = mma_desc(HT::kType, false, false, 128, 128);
         constexpr uint32_t d_pv = mma_desc(HT::kType, false, true, 128, DV);
-        constexpr uint32_t d_kv = mma_desc(HT::kType, true, true, 128, 2 * DV);
+        constexpr uint32_t d_kv = mma_desc(HT::kType, true, true, 128, HT::kParts * DV);
         constexpr int kTile = kBlockBytes >> 4, kRows = 2048 >> 4;  // to the next 64 elements, 16 rows
         const uint32_t base = smem_u32(smem);
         auto qd = [&](int s) { return tile_desc(base + s * kStageBytes, kBlockBytes); };
@@ -334,7 +344,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             const uint64_t vt = tile_desc(base + kOffVt, kBlockBytes), st = tile_desc(base + kOffS, kBlockBytes);
             for (int i = 0; i < n; ++i) {
                 const int s = i & 1;
-                // K^T [V~ high | V~ low] (side by side, added up by the state's warps) and Q S
+                // K^T [V~'s parts] (side by side, added up by the state's warps) and Q S
                 if (!wait(&sm.vt_full, i & 1) || !wait(&sm.full_qk[s], (i >> 1) & 1) ||
                     (i > 0 && !wait(&sm.kv_empty, (i - 1) & 1)))
                     break;
@@ -610,12 +620,16 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             const u64 lift2 = pk(lift, lift), f2 = pk(f, f);
 #pragma unroll
             for (int g = 0; g < DV; g += 16) {
-                uint32_t x[16], y[16];
-                tmem_ld16x2(tm + lanes + kKv + g, tm + lanes + kKv + DV + g, x, y);
+                uint32_t x[16], y[16], z[16];
+                if (HT::kParts == 3)
+                    tmem_ld16x3(tm + lanes + kKv + g, tm + lanes + kKv + DV + g, tm + lanes + kKv + 2 * DV + g, x, y, z);
+                else
+                    tmem_ld16x2(tm + lanes + kKv + g, tm + lanes + kKv + DV + g, x, y);
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
-                    u64 add = fadd2(pk(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
-                                    pk(__uint_as_float(y[j]), __uint_as_float(y[j + 1])));
+                    u64 add = pk(__uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                    if (HT::kParts == 3) add = fadd2(add, pk(__uint_as_float(z[j]), __uint_as_float(z[j + 1])));
+                    add = fadd2(add, pk(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
                     if (HT::kScaled) add = fmul2(add, lift2);
                     const u64 s2 = pk(S[g + j], S[g + j + 1]);
                     u64 to = ffma2(f2, s2, add);
@@ -685,11 +699,13 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                 const int at = (j ^ (row & 7)) << 4;
                 float f[8];
                 Vec16<T>::unpack(*reinterpret_cast<const uint4*>(vrow + at), f);
-                uint32_t h4[4], l4[4];
+                uint32_t part[4][HT::kParts];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) split2<T>(fmul2(factor2, pk(f[2 * u], f[2 * u + 1])), h4[u], l4[u]);
-                *reinterpret_cast<uint4*>(vt + row * 128 + at) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-                *reinterpret_cast<uint4*>(vt + kBlockBytes + row * 128 + at) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+                for (int u = 0; u < 4; ++u) split2<T>(fmul2(factor2, pk(f[2 * u], f[2 * u + 1])), part[u]);
+#pragma unroll
+                for (int u = 0; u < HT::kParts; ++u)
+                    *reinterpret_cast<uint4*>(vt + u * kBlockBytes + row * 128 + at) =
+                        make_uint4(part[0][u], part[1][u], part[2][u], part[3][u]);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -745,6 +761,7 @@ template <typename T>
 cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const ChunkArgs& a, int64_t grid,
                      cudaStream_t s) {
     auto* fn = linattn_chunk_kernel<T>;
+    constexpr int kSmem = Layout<T>::kSmem;
     int per_sm = 0;
     const cudaError_t e = prepared_launch(
         reinterpret_cast<const void*>(fn), kSmem, kThreads, &per_sm,
@@ -758,7 +775,7 @@ cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
 }  // namespace
 
 int linattn_chunk_block() { return kThreads; }
-int linattn_chunk_smem() { return kSmem; }
+int linattn_chunk_smem(int io_dt) { return io_dt == kF16 ? Layout<__half>::kSmem : Layout<__nv_bfloat16>::kSmem; }
 int linattn_chunk_tokens() { return C; }
 int linattn_chunk_values() { return DV; }
 uint64_t linattn_chunk_record_bytes() { return DV * C * 4; }

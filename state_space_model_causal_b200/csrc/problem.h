@@ -339,7 +339,7 @@ cudaError_t launch_linattn_generic(const LinAttnProblem& p, int rows, int grid, 
 int linattn_generic_block();
 int linattn_generic_rows(int64_t heads, int64_t P, int sms);  // rows of the state per CTA
 int linattn_chunk_block();
-int linattn_chunk_smem();
+int linattn_chunk_smem(int io_dt);
 int linattn_chunk_tokens();               // tokens per chunk
 int linattn_chunk_values();               // values per CTA
 uint64_t linattn_chunk_record_bytes();    // one state of a CTA

@@ -11,8 +11,8 @@ M.  u = eps / 2 is a type's unit, 2^-24 that of float32.
   itself is exp of a float32 number, 2 units at most per token: + 2 L 2^-24 M.
 * the chunk kernel rounds two factors of each product to the I/O type (scores,
   and the state that queries read): 2 u M for the output; its state sums
-  products with a weight split into two numbers of the I/O type, whose
-  remainder is below u^2 (bf16: 2^-16): + 2^-16 M.
+  products of weighted values split into numbers of the I/O type (two for f16,
+  three for bf16), whose remainder is at most u^2 (f16) or u^3 (bf16): + 2^-22 M.
 * an output is rounded to its type once: u |ref|.
 """
 import numpy as np
@@ -56,7 +56,7 @@ def bounds(q, k, v, g, s0, scale, lens, io, ref_out, chunk):
     f32 = (4 * L + N + 8) * 2.0 ** -24
     u = UNIT[io]
     out = u * np.abs(ref_out) + (f32 + (2 * u if chunk else 0.0)) * mo + TINY[io]
-    return out, (f32 + (2.0 ** -16 if chunk else 0.0)) * ms
+    return out, (f32 + (2.0 ** -22 if chunk else 0.0)) * ms
 
 
 def run(q, k, v, g, s0, scale=1.0, lens=None, io="f32", layout="token", workspace="auto"):
