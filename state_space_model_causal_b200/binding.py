@@ -286,8 +286,11 @@ def _pack_into(buf, offset, t):
     pack = _PACK.get(len(shape))
     if pack is None:
         raise ValueError(f"rank {t.dim()} is outside 1..{MAX_DIMS}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        code = _dtype_code(t)
     # an empty tensor's pointer may be NULL, which would mean "absent"
-    pack.pack_into(buf, offset, t.data_ptr() or 16, _dtype_code(t), len(shape), *shape, *t.stride())
+    pack.pack_into(buf, offset, t.data_ptr() or 16, code, len(shape), *shape, *t.stride())
 
 
 def describe(t) -> Tensor:
@@ -298,13 +301,17 @@ def describe(t) -> Tensor:
     return out
 
 
-def _make_args(cls, names, tensors, info=None):
-    """An args struct with its tensor fields filled in (None = absent)."""
+def _offsets(cls, *names):
+    return tuple(getattr(cls, name).offset for name in names)
+
+
+def _make_args(cls, offsets, tensors, info=None):
+    """An args struct with its tensor fields (by offset) filled in (None = absent)."""
     a = cls()
     a.struct_size = ctypes.sizeof(cls)
-    for name, t in zip(names, tensors):
+    for offset, t in zip(offsets, tensors):
         if t is not None:
-            _pack_into(a, getattr(cls, name).offset, t)
+            _pack_into(a, offset, t)
     if info is not None:
         a.info = _info_ptr(info)
     return a
@@ -487,6 +494,8 @@ def _workspace(dev, stream, nbytes):
 class _on_device:
     """Make `dev` current for the block (no-op when it already is)."""
 
+    __slots__ = ("dev", "ctx")
+
     def __init__(self, dev):
         self.dev = dev
         self.ctx = None
@@ -584,8 +593,9 @@ def _call_with_workspace(fn, size_fn, what, args, tensors, stream, workspace, op
     it; a captured graph gets one of its own), a uint8 CUDA tensor is passed
     as given, None passes none where the entry point can do without."""
     import torch
-    dev = device_of(tensors)
+    dev = device_of(tensors if workspace is None or isinstance(workspace, str) else (*tensors, workspace))
     with _on_device(dev):
+        handle = _stream_handle(dev, stream)
         ws = None
         if isinstance(workspace, str):
             if workspace != "auto":
@@ -596,16 +606,18 @@ def _call_with_workspace(fn, size_fn, what, args, tensors, stream, workspace, op
                 if stream is None:
                     ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
                 else:
-                    with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(dev, stream), device=dev)):
+                    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
                         ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
         elif workspace is not None:
-            device_of((*tensors, workspace))
             ws = workspace
         elif not optional:
             raise ValueError(f"{what} needs a workspace")
         if ws is not None:
             args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-        _check(_run(fn, args, tensors, stream), what)
+        _check(fn(ctypes.byref(args), handle), what)
+
+
+_LINATTN = _offsets(LinAttnArgs, "q", "k", "v", "log_decay", "state", "state_out", "seq_lens", "out")
 
 
 def ssm_linear_attention_fwd(q, k, v, log_decay, scale=1.0, state=None, state_out=None, seq_lens=None,
@@ -620,12 +632,16 @@ def ssm_linear_attention_fwd(q, k, v, log_decay, scale=1.0, state=None, state_ou
     if out is None:
         out = torch.empty_like(v)
     tensors = (q, k, v, log_decay, state, state_out, seq_lens, out)
-    a = _make_args(LinAttnArgs, ("q", "k", "v", "log_decay", "state", "state_out", "seq_lens", "out"), tensors, info)
+    a = _make_args(LinAttnArgs, _LINATTN, tensors, info)
     a.scale = scale
     lib = library()
     _call_with_workspace(lib.ssm_linear_attention_fwd, lib.ssm_linear_attention_workspace_size,
                          "ssm_linear_attention_fwd", a, tensors, stream, workspace, optional=True)
     return out
+
+
+_LINATTN_UPDATE = _offsets(LinAttnUpdateArgs, "state", "q", "k", "v", "log_decay", "state_batch_indices",
+                           "state_out", "out")
 
 
 def ssm_linear_attention_update(state, q, k, v, log_decay, scale=1.0, state_batch_indices=None,
@@ -638,11 +654,14 @@ def ssm_linear_attention_update(state, q, k, v, log_decay, scale=1.0, state_batc
     if out is None:
         out = torch.empty_like(v)
     tensors = (state, q, k, v, log_decay, state_batch_indices, state_out, out)
-    a = _make_args(LinAttnUpdateArgs, ("state", "q", "k", "v", "log_decay", "state_batch_indices", "state_out", "out"),
-                   tensors, info)
+    a = _make_args(LinAttnUpdateArgs, _LINATTN_UPDATE, tensors, info)
     a.scale = scale
     _check(_run(library().ssm_linear_attention_update, a, tensors, stream), "ssm_linear_attention_update")
     return out
+
+
+_PAGED = _offsets(PagedAttentionArgs, "q", "k_cache", "v_cache", "block_table", "seq_lens", "weights",
+                  "weights_out", "lse", "out")
 
 
 def ssm_paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, weights=None,
@@ -657,13 +676,16 @@ def ssm_paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, scale
     if out is None:
         out = torch.empty_like(q)
     tensors = (q, k_cache, v_cache, block_table, seq_lens, weights, weights_out, lse, out)
-    a = _make_args(PagedAttentionArgs, ("q", "k_cache", "v_cache", "block_table", "seq_lens", "weights", "weights_out",
-                                        "lse", "out"), tensors, info)
+    a = _make_args(PagedAttentionArgs, _PAGED, tensors, info)
     a.scale = q.shape[-1] ** -0.5 if scale is None else scale
     lib = library()
     _call_with_workspace(lib.ssm_paged_attention_decode, lib.ssm_paged_attention_workspace_size,
                          "ssm_paged_attention_decode", a, tensors, stream, workspace, optional=False)
     return out
+
+
+_EVICT = _offsets(KvEvictArgs, "k_cache", "v_cache", "weights", "block_table", "seq_lens", "new_block_table",
+                  "new_weights", "new_seq_lens", "kept")
 
 
 def ssm_kv_cache_evict(k_cache, v_cache, weights, block_table, seq_lens, new_block_table, keep, recent=0,
@@ -691,8 +713,7 @@ def ssm_kv_cache_evict(k_cache, v_cache, weights, block_table, seq_lens, new_blo
     if kept is None:
         kept = make((B, Hkv, keep), torch.int32)
     tensors = (k_cache, v_cache, weights, block_table, seq_lens, new_block_table, new_weights, new_seq_lens, kept)
-    a = _make_args(KvEvictArgs, ("k_cache", "v_cache", "weights", "block_table", "seq_lens", "new_block_table",
-                                 "new_weights", "new_seq_lens", "kept"), tensors, info)
+    a = _make_args(KvEvictArgs, _EVICT, tensors, info)
     a.keep, a.recent = keep, recent
     _check(_run(library().ssm_kv_cache_evict, a, tensors, stream), "ssm_kv_cache_evict")
     return new_seq_lens, kept, new_weights
