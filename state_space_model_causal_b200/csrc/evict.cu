@@ -53,18 +53,41 @@ __global__ void __launch_bounds__(kSelect) evict_select_kernel(const EvictProble
     const int first_recent = len - (int)(p.recent < n ? p.recent : n);
     const float* w = p.w + b * p.w_b + h * p.w_h;
     const int32_t* table = p.table + b * p.tb_b;
-    auto make_key = [&](int t) {
-        if (t >= len) return 0u;
-        const int32_t pg = table[(int64_t)(t / p.page) * p.tb_m];
-        return key_of(w[t * p.w_t], pg >= 0 && pg < p.pages, t >= first_recent);
+    // the keys of U tokens from t on, `step` apart (0 behind the end): loads of clamped
+    // addresses, all U in flight (behind a branch each waited for the one before)
+    auto make_keys = [&](int t, int step, auto& key) {
+        constexpr int U = sizeof(key) / 4;
+        int32_t pg[U];
+        float wv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = t + u * step < len ? t + u * step : len - 1;
+            pg[u] = table[(int64_t)(at / p.page) * p.tb_m];
+            wv[u] = w[at * p.w_t];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = t + u * step;
+            key[u] = at < len ? key_of(wv[u], pg[u] >= 0 && pg[u] < p.pages, at >= first_recent) : 0u;
+        }
+    };
+    auto make_key = [&](int t) {  // (t < len)
+        uint32_t key[1];
+        make_keys(t, 0, key);
+        return key[0];
     };
 
     if (CACHED) {
-#pragma unroll 8
-        for (int t = threadIdx.x; t < len; t += kSelect) keys[t] = make_key(t);
+        for (int t = threadIdx.x; t < len; t += 8 * kSelect) {
+            uint32_t key[8];
+            make_keys(t, kSelect, key);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (t + u * kSelect < len) keys[t + u * kSelect] = key[u];
+        }
         __syncthreads();
     }
-    auto key_at = [&](int t) { return CACHED ? (t < len ? keys[t] : 0u) : make_key(t); };
+    auto key_at = [&](int t) { return t < len ? (CACHED ? keys[t] : make_key(t)) : 0u; };
 
     // passes of 8 bits from the top; `left` tokens are still to be found among
     // the keys that agree with `prefix` in the bits above
@@ -83,10 +106,16 @@ __global__ void __launch_bounds__(kSelect) evict_select_kernel(const EvictProble
                 mine += key[u] != 0u;
                 const bool on = key[u] != 0u && (key[u] & above) == prefix;
                 if (!__any_sync(0xffffffffu, on)) continue;
-                // one atomic per distinct digit of the warp: softmax weights share their exponents
                 const uint32_t digit = on ? (key[u] >> shift) & 255u : 256u;
-                const uint32_t same = __match_any_sync(0xffffffffu, digit);
-                if (on && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+                if (shift == 24) {
+                    // one atomic per distinct digit of the warp: softmax weights share their exponents
+                    const uint32_t same = __match_any_sync(0xffffffffu, digit);
+                    if (on && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+                } else if (__all_sync(0xffffffffu, digit == __shfl_sync(0xffffffffu, digit, 0))) {
+                    if (lane == 0) atomicAdd(&hist[digit], 32u);  // (all equal: weights that never moved)
+                } else if (on) {
+                    atomicAdd(&hist[digit], 1u);
+                }
             }
         }
         if (shift == 24) {  // how many tokens there are, and how many stay
@@ -143,7 +172,7 @@ __global__ void __launch_bounds__(kSelect) evict_select_kernel(const EvictProble
         for (int i = 0; i < kItems; ++i) {
             const int t = t0 + threadIdx.x * kItems + i;
             const uint32_t key = key_at(t);
-            wv[i] = key >= prefix ? w[t * p.w_t] : 0.0f;  // (prefix > 0: the token is there)
+            wv[i] = w[(t < len ? t : len - 1) * p.w_t];
             gt[i] = key > prefix;
             eq[i] = key == prefix;
             ngt += gt[i];
@@ -186,18 +215,18 @@ __global__ void __launch_bounds__(kSelect) evict_select_kernel(const EvictProble
     if (h == 0 && threadIdx.x == 0) p.new_lens[b * p.nl_b] = (int32_t)stay;
 }
 
-// A CTA takes kRows kept tokens of one sequence for every head: first the offsets of
+// A CTA takes per_cta kept tokens of one sequence for every head: first the offsets of
 // their rows, one thread each (the table look-ups and their arithmetic once per
 // row), then the copy, consecutive threads on consecutive pieces of a row.  VEC: pieces
 // of 16 bytes (unit element stride, aligned rows), else single elements.
-constexpr int kRows = 32;
+constexpr int kRows = 32, kFewRows = 8;  // the latter while that leaves few CTAs
 
 template <typename W, bool VEC>
-__global__ void __launch_bounds__(kCopy) evict_copy_kernel(const EvictProblem p) {
+__global__ void __launch_bounds__(kCopy) evict_copy_kernel(const EvictProblem p, const int per_cta) {
     __shared__ int64_t k_from[kCopy], k_to[kCopy], v_from[kCopy], v_to[kCopy];  // element offsets, k_from < 0: no row
-    const int64_t blocks = (p.keep + kRows - 1) / kRows;
-    const int64_t b = blockIdx.x / blocks, j0 = (blockIdx.x - b * blocks) * kRows;
-    const int rows = (int)(p.keep - j0 < kRows ? p.keep - j0 : kRows);
+    const int64_t blocks = (p.keep + per_cta - 1) / per_cta;
+    const int64_t b = blockIdx.x / blocks, j0 = (blockIdx.x - b * blocks) * per_cta;
+    const int rows = (int)(p.keep - j0 < per_cta ? p.keep - j0 : per_cta);
     const int entries = rows * (int)p.Hkv;  // (Hkv < 2^26)
     const int pieces = VEC ? (int)(p.D * p.es / 16) : (int)p.D;
     const int per = VEC ? 16 / p.es : 1;  // elements per piece
@@ -255,7 +284,7 @@ __global__ void __launch_bounds__(kCopy) evict_copy_kernel(const EvictProblem p)
 }  // namespace
 
 int evict_select_block() { return kSelect; }
-int64_t evict_copy_ctas(int64_t keep) { return (keep + kRows - 1) / kRows; }
+int64_t evict_copy_ctas(int64_t keep) { return (keep + kFewRows - 1) / kFewRows; }
 
 cudaError_t launch_evict(const EvictProblem& p, bool vec, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
@@ -276,7 +305,8 @@ cudaError_t launch_evict(const EvictProblem& p, bool vec, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // the copy may be launched while the selection still runs; it waits for its results
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.Bn * evict_copy_ctas(p.keep)));
+    const int per_cta = p.Bn * ((p.keep + kRows - 1) / kRows) >= 512 ? kRows : kFewRows;
+    cfg.gridDim = dim3((unsigned)(p.Bn * ((p.keep + per_cta - 1) / per_cta)));
     cfg.blockDim = dim3(kCopy);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
@@ -284,9 +314,9 @@ cudaError_t launch_evict(const EvictProblem& p, bool vec, cudaStream_t s) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (vec) return cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint4, true>, p);
-    return p.es == 2 ? cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint16_t, false>, p)
-                     : cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint32_t, false>, p);
+    if (vec) return cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint4, true>, p, per_cta);
+    return p.es == 2 ? cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint16_t, false>, p, per_cta)
+                     : cudaLaunchKernelEx(&cfg, evict_copy_kernel<uint32_t, false>, p, per_cta);
 }
 
 }  // namespace ssm

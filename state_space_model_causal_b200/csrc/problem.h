@@ -362,7 +362,7 @@ int paged_heads_per_cta(int kernel, int64_t G);
 int paged_ctas_per_sm(int kernel, int64_t G, int64_t D);
 cudaError_t launch_evict(const EvictProblem& p, bool vec, cudaStream_t s);
 int evict_select_block();
-int64_t evict_copy_ctas(int64_t keep);  // CTAs of the copy per sequence
+int64_t evict_copy_ctas(int64_t keep);  // CTAs of the copy per sequence, at most
 cudaError_t launch_delta_sum(const DeltaSumProblem& p, int grid, int block, cudaStream_t s);
 cudaError_t launch_carry_fold(const CarryFoldProblem& p, int grid, int block, cudaStream_t s);
 int scan_m2_rows_per_cta(int64_t N);
