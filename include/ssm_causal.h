@@ -174,7 +174,7 @@ typedef enum ssm_kernel_id {
                                        tensor cores: 16-bit q, k, v, out with contiguous head
                                        dimensions, 16-byte aligned rows, key size <= 128 */
     SSM_KERNEL_LINATTN_GENERIC = 20, /* linear attention over a prompt, token by token: any
-                                       strides and types, a warp per 4 rows of the state */
+                                       strides and types, a warp per 4 or 2 rows of the state */
     SSM_KERNEL_LINATTN_STEP = 21,   /* linear attention of one token, 16-byte vectors of the state */
     SSM_KERNEL_LINATTN_STEP_GENERIC = 22, /* the same, any strides and sizes */
     SSM_KERNEL_PAGED_DECODE = 23,   /* paged attention of one token on the tensor cores: 16-bit,
@@ -535,9 +535,10 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  *
  * The chunk kernel's products are of 16-bit factors, summed in float32.  The
  * masked scores are rounded to q's dtype once (float16 with a power of two
- * taken out of every row, so that they cannot overflow); the state is held in
- * float32, and what is read from it or added to it is split into two 16-bit
- * numbers.
+ * taken out of every row, so that they cannot overflow), and so is the copy of the
+ * state that queries read.  The state itself is held in float32; what a token
+ * adds to it enters as a sum of 16-bit numbers (two for float16, three for
+ * bfloat16), which loses at most 2^-22 of it.
  *
  * The workspace holds the end states of the pieces that few long sequences
  * are cut into: ssm_linear_attention_workspace_size() returns its size in bytes
@@ -729,12 +730,13 @@ ssm_status ssm_kv_cache_evict(const ssm_kv_evict_args* args, void* stream);
  *     unit's later outputs and final state are wrong, all other units are
  *     complete.
  *   ssm_linear_attention_update (SSM_KERNEL_LINATTN_STEP_BULK): the CTA that gave up
- *     exits, what it had not finished neither updated nor written; first_item
- *     is its number.
+ *     exits; of the work items it had not finished the states may be advanced and
+ *     outputs written in part.  first_item is the lowest such item: batch-major,
+ *     then head, then block of rows_per_item rows.
  *   ssm_linear_attention_fwd (SSM_KERNEL_LINATTN_CHUNK): the CTA that gave up
- *     exits, its later outputs and its state not written; first_item is its
- *     number, (b * H + h) * ceil(P / 64) + value block, times the pieces its
- *     sequences are cut into, plus its piece.
+ *     exits, its later outputs and its state not written; first_item is
+ *     (b * H + h) * ceil(P / 64) + value block; where sequences are cut into
+ *     pieces, times pieces - 1 plus the piece, less 1 in the second launch.
  *   ssm_selective_scan_fwd, x of rank 4 (SSM_KERNEL_SCAN_M2): the same for a
  *     CTA that waited in vain for its predecessor's state tile; first_item is
  *     the unit (b * H + h) * ceil(P / rows per CTA) + row block.

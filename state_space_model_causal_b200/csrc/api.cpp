@@ -390,11 +390,6 @@ ssm_status gated_conv_impl(const ssm_gated_conv1d_args* a, cudaStream_t stream) 
 // Balanced prefill workspace: a 256-byte header (generation, finished-worker
 // count), one 32-bit flag per worker (rounded up to 256 bytes), then one
 // hand-over state of 16 channels x 16 state entries (1 KB) per worker.
-constexpr long long kWaitBudget = 4000000000LL;  // cycles (~2 s) before a bounded wait gives up
-constexpr long long kMinTestBudget = 10000000LL; // shortest wait a failure test may ask for
-
-// A failure test's wait budget, never below kMinTestBudget.
-long long clamp_test_budget(long long v) { return v < kMinTestBudget ? kMinTestBudget : v; }
 uint64_t bal_flag_bytes(int64_t workers) { return ((uint64_t)workers * 4 + 255) / 256 * 256; }
 // bytes of one hand-over slot: a unit's 16 x 16 state and 16 partial sums of delta
 uint64_t bal_slot_bytes() { return (uint64_t)scan_bal_channels_per_unit() * 17 * 4; }

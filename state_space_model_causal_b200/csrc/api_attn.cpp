@@ -17,9 +17,18 @@ namespace {
 using namespace ssm;
 
 constexpr int kMaxN = 256;  // keys per state row, elements per head
-constexpr long long kWaitBudget = 4000000000LL;  // cycles (~2 s) before a bounded wait gives up
 
 uint64_t round256(uint64_t v) { return (v + 255) / 256 * 256; }
+
+BoundedWaits bounded_waits() {
+    BoundedWaits w{kWaitBudget, -1};
+#ifdef SSM_TEST_HOOKS
+    long long v = 0;
+    if (env_int("SSM_TEST_WAIT_CYCLES", &v) && v > 0) w.budget = clamp_test_budget(v);
+    if (env_int("SSM_TEST_DROP_ITEM", &v) && v >= 0) w.drop_item = v;
+#endif
+    return w;
+}
 
 bool same_view(const ssm_tensor& a, const ssm_tensor& b) {
     if (a.data != b.data || a.dtype != b.dtype || a.ndim != b.ndim) return false;
@@ -174,12 +183,12 @@ ssm_status linattn_impl(const ssm_linattn_args* a, cudaStream_t stream, uint64_t
                 if (present(*t) && overlap(ws, *t)) return SSM_ERR_ALIAS;
         }
         if (units > INT32_MAX / pieces) return SSM_ERR_UNSUPPORTED;
-        fill_info(a->info, SSM_KERNEL_LINATTN_CHUNK, (int)(units * std::max<int64_t>(pieces - 1, 1)), linattn_chunk_block(), linattn_chunk_smem(io),
-                  linattn_chunk_values(), units * pieces);
+        fill_info(a->info, SSM_KERNEL_LINATTN_CHUNK, (int)(units * std::max<int64_t>(pieces - 1, 1)), linattn_chunk_block(),
+                  linattn_chunk_smem(io), linattn_chunk_values(), units * pieces);
         if (dry) return SSM_OK;
         char* ws = static_cast<char*>(a->workspace);
         return launch_linattn_chunk(p, units, cut, reinterpret_cast<float*>(ws),
-                                    reinterpret_cast<double*>(ws + rec), kWaitBudget, dev, stream) == cudaSuccess
+                                    reinterpret_cast<double*>(ws + rec), bounded_waits(), dev, stream) == cudaSuccess
                    ? SSM_OK : SSM_ERR_CUDA;
     }
     const int64_t rows = linattn_generic_rows(B * H, P, sm_count(dry)), blocks = (P + rows - 1) / rows;
@@ -245,7 +254,14 @@ ssm_status linattn_update_impl(const ssm_linattn_update_args* a, cudaStream_t st
     const int kernel = bulk ? SSM_KERNEL_LINATTN_STEP_BULK : vec ? SSM_KERNEL_LINATTN_STEP : SSM_KERNEL_LINATTN_STEP_GENERIC;
     const bool dry = (a->flags & SSM_FLAG_DRY_RUN) != 0;
     const int dev = current_device(dry), sms = sm_count(dry, dev);
-    fill_info(a->info, kernel, bulk ? std::min(items, 2 * sms) : items, linattn_step_block(), 0, rows, items);
+    LinAttnStepBulk plan{};
+    if (bulk) {
+        plan = linattn_step_bulk_plan(st, B * H, P, N, sms);
+        fill_info(a->info, kernel, (int)plan.grid, linattn_step_block(), plan.smem, (int64_t)plan.rows * plan.blocks,
+                  plan.units);
+    } else {
+        fill_info(a->info, kernel, items, linattn_step_block(), 0, rows, items);
+    }
     if (dry) return SSM_OK;
 
     LinAttnStepProblem p{};
@@ -266,7 +282,7 @@ ssm_status linattn_update_impl(const ssm_linattn_update_args* a, cudaStream_t st
     }
     p.scale = a->scale;
     p.out = a->out.data; p.o_b = sd(a->out, 0); p.o_h = sd(a->out, 1); p.o_p = sd(a->out, 2);
-    const cudaError_t e = bulk ? launch_linattn_step_bulk(p, sms, dev, kWaitBudget, stream)
+    const cudaError_t e = bulk ? launch_linattn_step_bulk(p, plan, bounded_waits(), dev, stream)
                                : launch_linattn_step(p, kernel, items, stream);
     return e == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }

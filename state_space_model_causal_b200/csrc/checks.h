@@ -146,6 +146,12 @@ inline bool env_int(const char* name, long long* v) {
     return true;
 }
 
+constexpr long long kWaitBudget = 4000000000LL;  // cycles (~2 s) before a bounded wait gives up
+constexpr long long kMinTestBudget = 10000000LL; // shortest wait a failure test may ask for
+
+// A failure test's wait budget, never below kMinTestBudget.
+inline long long clamp_test_budget(long long v) { return v < kMinTestBudget ? kMinTestBudget : v; }
+
 // The current device (0 in dry-run mode, which makes no CUDA call).
 inline int current_device(bool dry_run) {
     int dev = 0;

@@ -258,15 +258,12 @@ struct BulkSmem {
     int64_t slot[kStages];
     float v[2][kUnitRows];
 };
-struct BulkShape {
-    uint32_t units;       // (b, h, group of blocks)
-    uint32_t groups;      // groups per head
-    int rows, blocks;     // rows per block, blocks per group
-};
+constexpr int kBulkCtas = 4;  // per SM
+static_assert(kBulkCtas * (sizeof(BulkSmem) + 1024) <= 228 * 1024, "shared memory of an SM");
 
 template <typename ST, int CPL>
-__global__ void __launch_bounds__(kBlock, 4) linattn_step_bulk_kernel(const LinAttnStepProblem p, const BulkShape sh,
-                                                                   DeviceError* err, long long wait_budget) {
+__global__ void __launch_bounds__(kBlock, kBulkCtas)
+linattn_step_bulk_kernel(const LinAttnStepProblem p, const LinAttnStepBulk sh, DeviceError* err, const BoundedWaits waits) {
     constexpr int VE = Vec16<ST>::VE, VN = kUnitRows / kBlock, RU = StepShape<CPL>::RU;
     extern __shared__ __align__(128) unsigned char raw[];
     BulkSmem& sm = *reinterpret_cast<BulkSmem*>(raw);
@@ -295,6 +292,9 @@ __global__ void __launch_bounds__(kBlock, 4) linattn_step_bulk_kernel(const LinA
     int64_t ahead_slot = -1;
     auto fetch = [&] {
         if (ahead_unit >= sh.units) return;
+#ifdef SSM_TEST_HOOKS
+        if ((int64_t)ahead_unit == waits.drop_item) return;  // never issued
+#endif
         if (ahead_block == 0) {
             ahead = unit_at(ahead_unit);
             ahead_slot = p.slot_idx ? p.slot_idx[ahead.b * p.ix_b] : ahead.b;
@@ -352,7 +352,9 @@ __global__ void __launch_bounds__(kBlock, 4) linattn_step_bulk_kernel(const LinA
     }
     __syncthreads();
     bool ok = true;
+    uint32_t unit = u;
     for (int buf = 0; ok && u < sh.units; buf ^= 1) {
+        unit = u;
         const Unit t = next;
         float kf[CPL][VE], qf[CPL][VE];
 #pragma unroll
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kBlock, 4) linattn_step_bulk_kernel(const LinA
         for (int blk = 0; blk < t.blocks; ++blk, ++done) {
             const int s = (int)(done % kStages), r0 = blk * sh.rows;
             const int rows = t.rows - r0 < sh.rows ? t.rows - r0 : sh.rows;
-            const bool here = mbar_wait_bounded(&sm.full[s], (done / kStages) & 1, wait_budget);
+            const bool here = mbar_wait_bounded(&sm.full[s], (done / kStages) & 1, waits.budget);
             const int64_t slot = sm.slot[s];
             if (here && slot >= 0) {
                 // RU groups of rows at a time: their loads together, their sums together
@@ -434,8 +436,8 @@ __global__ void __launch_bounds__(kBlock, 4) linattn_step_bulk_kernel(const LinA
     }
     if (threadIdx.x == 0) {
         if (!ok) {  // a copy never came: leave with none in flight
-            report_device_error(err, SSM_KERNEL_LINATTN_STEP_BULK, (long long)blockIdx.x);
-            for (; done < issued; ++done) mbar_wait_bounded(&sm.full[done % kStages], (done / kStages) & 1, wait_budget);
+            report_device_error(err, SSM_KERNEL_LINATTN_STEP_BULK, (long long)unit);
+            for (; done < issued; ++done) mbar_wait_bounded(&sm.full[done % kStages], (done / kStages) & 1, waits.budget);
         }
         bulk_wait_all();
     }
@@ -473,29 +475,16 @@ cudaError_t step_t(const LinAttnStepProblem& p, int grid, cudaStream_t s) {
 }
 
 template <typename ST, int CPL>
-cudaError_t bulk_t(const LinAttnStepProblem& p, int sms, int rows, DeviceError* err, long long budget, cudaStream_t s) {
+cudaError_t bulk_t(const LinAttnStepProblem& p, const LinAttnStepBulk& plan, DeviceError* err, const BoundedWaits& waits,
+                   cudaStream_t s) {
     auto* fn = linattn_step_bulk_kernel<ST, CPL>;
-    constexpr int smem = (int)sizeof(BulkSmem);
     int per_sm = 0;
     const cudaError_t e = prepared_launch(
-        reinterpret_cast<const void*>(fn), smem, kBlock, &per_sm,
+        reinterpret_cast<const void*>(fn), plan.smem, kBlock, &per_sm,
         [&](int bytes) { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); },
-        [&](int* n) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, fn, kBlock, smem); });
+        [&](int* n) { *n = kBulkCtas; return cudaSuccess; });
     if (e != cudaSuccess) return e;
-    const int64_t wave = (int64_t)sms * (per_sm > 0 ? per_sm : 1), heads = p.Bn * p.H;
-    const int64_t per_head = (p.P + rows - 1) / rows;
-    // as many blocks per unit as leave every CTA four units or more
-    int64_t blocks = heads * per_head / (4 * wave);
-    blocks = blocks < 1 ? 1 : blocks;
-    blocks = blocks > per_head ? per_head : blocks;
-    if (blocks * rows > kUnitRows) blocks = kUnitRows / rows;
-    BulkShape sh;
-    sh.rows = rows;
-    sh.blocks = (int)blocks;
-    sh.groups = (uint32_t)((per_head + blocks - 1) / blocks);
-    sh.units = (uint32_t)(heads * sh.groups);
-    const int64_t grid = sh.units < wave ? sh.units : wave;
-    fn<<<(unsigned)grid, kBlock, smem, s>>>(p, sh, err, budget);
+    fn<<<plan.grid, kBlock, plan.smem, s>>>(p, plan, err, waits);
     return cudaGetLastError();
 }
 
@@ -532,14 +521,30 @@ int linattn_step_bulk_rows(int st_dt, int64_t N) {
     return (int)(rows < kUnitRows ? rows : kUnitRows);
 }
 
-cudaError_t launch_linattn_step_bulk(const LinAttnStepProblem& p, int sms, int dev, long long wait_budget, cudaStream_t s) {
+LinAttnStepBulk linattn_step_bulk_plan(int st_dt, int64_t heads, int64_t P, int64_t N, int sms) {
+    LinAttnStepBulk plan;
+    plan.smem = (int)sizeof(BulkSmem);
+    plan.rows = linattn_step_bulk_rows(st_dt, N);
+    const int64_t wave = (int64_t)sms * kBulkCtas, per_head = (P + plan.rows - 1) / plan.rows;
+    // as many blocks per unit as leave every CTA four units or more
+    int64_t blocks = heads * per_head / (4 * wave);
+    blocks = blocks < 1 ? 1 : blocks;
+    blocks = blocks > per_head ? per_head : blocks;
+    if (blocks * plan.rows > kUnitRows) blocks = kUnitRows / plan.rows;
+    plan.blocks = (int)blocks;
+    plan.groups = (uint32_t)((per_head + blocks - 1) / blocks);
+    plan.units = (uint32_t)(heads * plan.groups);
+    plan.grid = plan.units < wave ? plan.units : (uint32_t)wave;
+    return plan;
+}
+
+cudaError_t launch_linattn_step_bulk(const LinAttnStepProblem& p, const LinAttnStepBulk& plan, const BoundedWaits& waits,
+                                     int dev, cudaStream_t s) {
     DeviceError* err = device_error_ptr(dev);
     if (!err) return cudaErrorUnknown;
-    const int rows = linattn_step_bulk_rows(p.st_dt, p.N);
-    if (p.st_dt == kF16) return bulk_t<__half, 1>(p, sms, rows, err, wait_budget, s);
-    if (p.st_dt == kBF16) return bulk_t<__nv_bfloat16, 1>(p, sms, rows, err, wait_budget, s);
-    return p.N <= 128 ? bulk_t<float, 1>(p, sms, rows, err, wait_budget, s)
-                      : bulk_t<float, 2>(p, sms, rows, err, wait_budget, s);
+    if (p.st_dt == kF16) return bulk_t<__half, 1>(p, plan, err, waits, s);
+    if (p.st_dt == kBF16) return bulk_t<__nv_bfloat16, 1>(p, plan, err, waits, s);
+    return p.N <= 128 ? bulk_t<float, 1>(p, plan, err, waits, s) : bulk_t<float, 2>(p, plan, err, waits, s);
 }
 
 cudaError_t launch_linattn_step(const LinAttnStepProblem& p, int kernel, int grid, cudaStream_t s) {

@@ -119,7 +119,7 @@ struct ChunkArgs {
     float* rec;          // [unit][pieces - 1][64 values][128 keys]: end of the piece (from zero, but for 0)
     double* rec_g;       // [unit][pieces - 1]: log2 of the piece's decay
     DeviceError* err;
-    long long wait_budget;
+    BoundedWaits waits;
 };
 
 // Bounded wait; a wait that runs out ends every role of the CTA.
@@ -141,7 +141,7 @@ struct Waiter {
     const ChunkArgs* a;
     // by one thread
     __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
-        return mbar_try(bar, parity) || wait_long(bar, parity, &sm->abort, a->err, a->wait_budget);
+        return mbar_try(bar, parity) || wait_long(bar, parity, &sm->abort, a->err, a->waits.budget);
     }
     // by a whole warp, with one answer
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
@@ -260,8 +260,6 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     auto k_tile = [&](int s) { return smem + s * kStageBytes + 2 * kBlockBytes; };
     auto v_tile = [&](int s) { return smem + s * kStageBytes + 4 * kBlockBytes; };
 
-    // the largest value (>= 0) of a warpgroup; both groups that ask, the state's and the
-        // values', have a place of their own
     // the largest exponent in a warpgroup (group 0: the state's, 1: the values'), at its call i
     auto group_max = [&](float v, int group, int i, uint32_t& top) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, exponent_of(v));
@@ -282,6 +280,9 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             const int hk = (int)(h / p.rep);
             int issued = 0;
             for (int i = 0; i < n; ++i, ++issued) {
+#ifdef SSM_TEST_HOOKS
+                if ((int64_t)blockIdx.x == a.waits.drop_item) break;  // never issued
+#endif
                 const int s = i & 1;
                 const uint32_t reuse = ((i >> 1) & 1) ^ 1;
                 const int t = (int)((c0 + i) * C);
@@ -294,7 +295,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                     tma_load_4d(q_tile(s) + kBlockBytes, &mq, 64, t, hk, (int)b, &sm.full_qk[s]);
                 }
                 if (i >= 2 && !wait.one(&sm.empty_v[s], reuse)) {  // (its Q, K are in flight)
-                    mbar_wait_bounded(&sm.full_qk[s], (i >> 1) & 1, a.wait_budget);
+                    mbar_wait_bounded(&sm.full_qk[s], (i >> 1) & 1, a.waits.budget);
                     break;
                 }
                 mbar_arrive_expect_tx(&sm.full_v[s], kBlockBytes);
@@ -302,8 +303,8 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             }
             if (*(volatile int*)&sm.abort)  // leave with no copy in flight
                 for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i) {
-                    mbar_wait_bounded(&sm.full_qk[i & 1], (i >> 1) & 1, a.wait_budget);
-                    mbar_wait_bounded(&sm.full_v[i & 1], (i >> 1) & 1, a.wait_budget);
+                    mbar_wait_bounded(&sm.full_qk[i & 1], (i >> 1) & 1, a.waits.budget);
+                    mbar_wait_bounded(&sm.full_v[i & 1], (i >> 1) & 1, a.waits.budget);
                 }
         }
     } else if (warp == 1 || warp == 3) {
@@ -366,7 +367,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         // every product done before tensor memory is freed
         if (start && n > 0 && (warp == 3 || outputs)) {
             mma_commit(&sm.spare);
-            mbar_wait_bounded(&sm.spare, 0, a.wait_budget);
+            mbar_wait_bounded(&sm.spare, 0, a.waits.budget);
         }
     } else if (warp == 2) {
         // -------------------------------------------------------- decay sums --
@@ -781,7 +782,7 @@ int linattn_chunk_values() { return DV; }
 uint64_t linattn_chunk_record_bytes() { return DV * C * 4; }
 
 cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, const LinAttnPieces& cut, float* rec, double* rec_g,
-                                 long long wait_budget, int dev, cudaStream_t s) {
+                                 const BoundedWaits& waits, int dev, cudaStream_t s) {
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, p.io_dt, p.q, p.N, p.L, p.Hk, p.Bn, p.q_t, p.q_h, p.q_b) ||
         !make_map(&mk, p.io_dt, p.k, p.N, p.L, p.Hk, p.Bn, p.k_t, p.k_h, p.k_b) ||
@@ -799,7 +800,7 @@ cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, const L
               p.o_t % 16 == 0;
     a.err = device_error_ptr(dev);
     if (!a.err) return cudaErrorUnknown;
-    a.wait_budget = wait_budget;
+    a.waits = waits;
     const bool f16 = p.io_dt == kF16;
     const int64_t grid = cut.pieces > 1 ? units * (cut.pieces - 1) : units;
     if (cut.pieces > 1) {

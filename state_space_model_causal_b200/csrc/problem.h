@@ -281,6 +281,11 @@ struct PagedProblem {
     float* ws_s;          // [b][hq][cap]: scores in log2 (with weights)
 };
 
+struct BoundedWaits {
+    long long budget;   // cycles before a wait gives up
+    int64_t drop_item;  // failure tests only: work item whose copies are never started (-1: none)
+};
+
 // Eviction: the selection writes `kept`, new_w and new_lens, the copy follows it.
 struct EvictProblem {
     int64_t Bn, Hkv, D, pages, M, M2, cap;
@@ -349,10 +354,18 @@ struct LinAttnPieces {
 };
 // pieces > 1: rec holds units * (pieces - 1) records, rec_g as many doubles
 cudaError_t launch_linattn_chunk(const LinAttnProblem& p, int64_t units, const LinAttnPieces& cut, float* rec, double* rec_g,
-                                 long long wait_budget, int dev, cudaStream_t s);
+                                 const BoundedWaits& waits, int dev, cudaStream_t s);
 cudaError_t launch_linattn_step(const LinAttnStepProblem& p, int kernel, int grid, cudaStream_t s);
-int linattn_step_bulk_rows(int st_dt, int64_t N);  // rows of the state per item of the bulk-copy kernel
-cudaError_t launch_linattn_step_bulk(const LinAttnStepProblem& p, int sms, int dev, long long wait_budget, cudaStream_t s);
+int linattn_step_bulk_rows(int st_dt, int64_t N);  // rows of the state per block of the bulk-copy kernel
+struct LinAttnStepBulk {
+    uint32_t grid, units;  // a unit: (b, h, group of blocks)
+    uint32_t groups;       // groups per head
+    int rows, blocks;      // rows per block, blocks per group
+    int smem;
+};
+LinAttnStepBulk linattn_step_bulk_plan(int st_dt, int64_t heads, int64_t P, int64_t N, int sms);
+cudaError_t launch_linattn_step_bulk(const LinAttnStepProblem& p, const LinAttnStepBulk& plan, const BoundedWaits& waits,
+                                     int dev, cudaStream_t s);
 int linattn_step_block();
 int linattn_step_rows(int st_dt, int64_t N, bool vec);  // rows of the state per CTA
 cudaError_t launch_paged(const PagedProblem& p, int kernel, cudaStream_t s);
