@@ -528,7 +528,8 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  *
  * Any strides.  16-bit types with unit strides along N and P, N <= 128, N and P
  * multiples of 8 and 16-byte aligned rows run on SSM_KERNEL_LINATTN_CHUNK (the
- * rows of a token-major projection seen as (B, H, L, N) count); everything
+ * rows of a token-major projection seen as (B, H, L, N) count; broadcast
+ * dimensions do not); everything
  * else on SSM_KERNEL_LINATTN_GENERIC.  L = 0, like a seq_len of 0, copies state
  * to state_out.  out and state_out may not overlap an input; state_out is
  * either exactly `state` or does not overlap it.
@@ -538,7 +539,9 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  * taken out of every row, so that they cannot overflow), and so is the copy of the
  * state that queries read.  The state itself is held in float32; what a token
  * adds to it enters as a sum of 16-bit numbers (two for float16, three for
- * bfloat16), which loses at most 2^-22 of it.
+ * bfloat16), which loses at most 2^-22 of it.  An infinity counts as a NaN there:
+ * one in v makes its column of the outputs from its token on, and of the state, NaN,
+ * one in k every output from its token on.
  *
  * The workspace holds the end states of the pieces that few long sequences
  * are cut into: ssm_linear_attention_workspace_size() returns its size in bytes

@@ -40,6 +40,7 @@
 // chunks.  A first launch computes piece 0, and of the others but the last the end
 // states from zero (keys and values only, which takes half as long: piece 0 is half as
 // long as the others); a second starts pieces 1, 2, ... from the states composed of those.
+#include <climits>
 #include <type_traits>
 
 #include "../../include/ssm_causal.h"
@@ -88,8 +89,12 @@ struct Small {
     uint64_t g_full[2], g_empty[2];                           // decay sums
     uint64_t sc_full, top_full;                               // scores' accumulator; f16: their largest
     uint64_t p_full, vt_full, kv_full, kv_empty, s_full, qs_done, o_full, o_empty, red_full[2], spare;
+    uint64_t v_read[2], out_done, state_done, repaired, repair_sync;
     uint32_t tmem;
     int abort;
+    int not_finite;            // the state at the end
+    float part[4];             // of a sum, per warp
+    int first[4];              // a token, per warp
     uint8_t red[2][2][4];      // f16: exponents of the largest values, per warp
     int s_lift[2], v_lift[2];  // f16: S, V~ were divided by 2^lift
     static constexpr int kRows = Half16<T>::kScaled ? C : 1;
@@ -176,6 +181,37 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
                  : "memory");
 }
 
+// What a CTA does.
+struct Place {
+    int64_t unit, b, h;
+    int piece, p0;   // p0: first value
+    int64_t len;     // tokens of the sequence
+    int64_t c0;      // first chunk
+    int chunks;
+};
+__device__ __forceinline__ Place place_of(const ChunkArgs& a, uint32_t block) {
+    const LinAttnProblem& p = a.p;
+    Place at;
+    const int n_pieces = a.phase == 0 ? 1 : a.pieces - 1;
+    at.unit = block / n_pieces;
+    at.piece = (int)(block - at.unit * n_pieces) + (a.phase == 2 ? 1 : 0);
+    const int64_t bh = at.unit / a.pt;
+    at.b = bh / p.H;
+    at.h = bh - at.b * p.H;
+    at.p0 = (int)(at.unit - bh * a.pt) * DV;
+    at.len = p.L;
+    if (p.lens) {
+        const int64_t n = p.lens[at.b * p.len_b];
+        at.len = n < 0 ? 0 : (n < p.L ? n : p.L);
+    }
+    const int64_t seq_chunks = (at.len + C - 1) / C;
+    at.c0 = at.piece == 0 ? 0 : a.piece0 + (at.piece - 1) * a.per_piece;
+    int64_t c1 = at.piece == 0 ? a.piece0 : at.c0 + a.per_piece;
+    if (c1 > seq_chunks) c1 = seq_chunks;
+    at.chunks = c1 > at.c0 ? (int)(c1 - at.c0) : 0;
+    return at;
+}
+
 // Registers per thread: 96 at launch (640 threads), of which the warpgroup that holds the
 // state takes 128 and the others keep 88.
 constexpr int kRegs = 88, kRegsState = 128;
@@ -202,23 +238,11 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     Small<T>& sm = *reinterpret_cast<Small<T>*>(smem + Layout<T>::kTiles);
     const LinAttnProblem& p = a.p;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int n_pieces = a.phase == 0 ? 1 : a.pieces - 1;
-    const int64_t unit = blockIdx.x / n_pieces;
-    const int piece = (int)(blockIdx.x - unit * n_pieces) + (a.phase == 2 ? 1 : 0);
-    const int64_t bh = unit / a.pt, b = bh / p.H, h = bh - b * p.H;
-    const int p0 = (int)(unit - bh * a.pt) * DV;
+    const Place at = place_of(a, blockIdx.x);
+    const int64_t unit = at.unit, b = at.b, h = at.h, len = at.len, c0 = at.c0;
+    const int piece = at.piece, p0 = at.p0, n = at.chunks;
     const bool outputs = a.phase != 1 || piece == 0;
 
-    int64_t len = p.L;
-    if (p.lens) {
-        const int64_t n = p.lens[b * p.len_b];
-        len = n < 0 ? 0 : (n < p.L ? n : p.L);
-    }
-    const int64_t seq_chunks = (len + C - 1) / C;
-    const int64_t c0 = piece == 0 ? 0 : a.piece0 + (piece - 1) * a.per_piece;
-    int64_t c1 = piece == 0 ? a.piece0 : c0 + a.per_piece;
-    if (c1 > seq_chunks) c1 = seq_chunks;
-    const int n = c1 > c0 ? (int)(c1 - c0) : 0;  // this CTA's chunks
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -241,6 +265,13 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         mbar_init(&sm.o_empty, 4);
         mbar_init(&sm.red_full[0], 4);
         mbar_init(&sm.red_full[1], 4);
+        mbar_init(&sm.v_read[0], 4);
+        mbar_init(&sm.v_read[1], 4);
+        mbar_init(&sm.out_done, 4);
+        mbar_init(&sm.state_done, 4);
+        mbar_init(&sm.repaired, 4);
+        mbar_init(&sm.repair_sync, 4);
+        sm.not_finite = 0;
         mbar_init(&sm.spare, outputs ? 2 : 1);
         sm.abort = (smem_u32(smem) & 1023u) != 0;  // the swizzle counts from 1024-byte boundaries
         if (sm.abort) report_device_error(a.err, SSM_KERNEL_LINATTN_CHUNK, (long long)blockIdx.x);
@@ -325,8 +356,9 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             for (int i = -1; i < n; ++i) {
                 const int s = i & 1, j = i + 1, js = j & 1;
                 if (i >= 0) {
-                    // (V~ made: rows behind the end are 0 by then, in V too)
-                    if (!wait(&sm.full_v[s], (i >> 1) & 1) || !wait(&sm.vt_full, i & 1) || !wait(&sm.p_full, i & 1) ||
+                    // (V~ made: rows behind the end are 0 by then, in V too.  A barrier per stage:
+                    // the next chunk's V~ may be made before this warp looks)
+                    if (!wait(&sm.full_v[s], (i >> 1) & 1) || !wait(&sm.v_read[s], (i >> 1) & 1) || !wait(&sm.p_full, i & 1) ||
                         (i > 0 && !wait(&sm.o_empty, (i - 1) & 1)))
                         break;
                     tc_fence_after();
@@ -539,6 +571,8 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             }
             if (group && !output(i, ex2_approx(hi) * p.scale)) break;
         }
+        __syncwarp();
+        if (group && lane == 0) mbar_arrive(&sm.out_done);
     } else if (warp >= 8 && warp < 12) {
         // ------------------------------------------------------------- state --
         more_registers<kRegsState>();
@@ -602,7 +636,8 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             return true;
         };
         double total = 0.0;
-        for (int i = 0; start && i < n; ++i) {
+        int i = 0;
+        for (; start && i < n; ++i) {
             const int s = i & 1;
             if (outputs && !((i == 0 || wait(&sm.qs_done, (i - 1) & 1)) && put_state(i))) break;
             if (!wait(&sm.g_full[s], (i >> 1) & 1)) break;
@@ -642,11 +677,27 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.kv_empty);
         }
-        if (start && a.phase == 1) {
+        bool done = start && i == n;  // (no wait ran out)
+        if (done && outputs && n > 0) {
+            u64 zeros = 0;  // 0 times every number of S: a NaN if one is not finite
+#pragma unroll
+            for (int j = 0; j < DV; j += 2) zeros = ffma2(pk(S[j], S[j + 1]), 0, zeros);
+            float z0, z1;
+            upk(zeros, z0, z1);
+            if (z0 + z1 != 0.0f) *(volatile int*)&sm.not_finite = 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.state_done);
+            done = wait(&sm.state_done, 0);
+            // (the repair works longer than a wait may take, and ends this one if it gives up)
+            if (done && *(volatile int*)&sm.not_finite)
+                done = __all_sync(0xffffffffu, wait_long(&sm.repaired, 0, &sm.abort, a.err, DV * a.waits.budget));
+        }
+        if (!done) {  // nothing to hand on
+        } else if (a.phase == 1) {
 #pragma unroll
             for (int j = 0; j < DV; ++j) rec[piece * (DV * C) + j * C] = S[j];
             if (row == 0) a.rec_g[unit * (a.pieces - 1) + piece] = total;
-        } else if (start && p.s_out && piece == a.pieces - 1 && key) {
+        } else if (p.s_out && piece == a.pieces - 1 && key) {
             float* at = p.s_out + b * p.so_b + h * p.so_h + p0 * p.so_p + row * p.so_n;
 #pragma unroll
             for (int j = 0; j < DV; ++j) {
@@ -712,13 +763,88 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sm.vt_full);
+                mbar_arrive(&sm.v_read[s]);
                 mbar_arrive(&sm.empty_v[s]);
                 mbar_arrive(&sm.g_empty[s]);
             }
             return true;
         };
-        for (int i = 0; start && i < n; ++i)
-            if (!values(i)) break;
+        int syncs = 0;
+        // the four warps of this group, waiting for one another
+        auto sync = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.repair_sync);
+            return wait(&sm.repair_sync, syncs++ & 1);
+        };
+        // A weight of 0 does not keep a NaN or an infinity of V from the tokens before it
+        // in a product: its column is NaN from the first token of its chunk on, and so is the
+        // state.  When the state ends up like that, the outputs between that token and the
+        // first value that is not finite are computed again, token by token (before the new
+        // state is written, which may be where the old one is).  Looking at every value of V
+        // instead took 4 to 8% of the kernel's time, in whichever warps; this takes 2 to 3.
+        auto repair = [&] {
+            if (!wait(&sm.out_done, 0)) return false;
+            // (found again: kept, these would take registers from the loops above)
+            uint32_t block;
+            asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(block));
+            const Place at = place_of(a, block);
+            const int64_t unit = at.unit, b = at.b, h = at.h, end = (at.c0 + at.chunks) * C;
+            const int piece = at.piece, p0 = at.p0, t0 = (int)(at.c0 * C), t1 = (int)(end < at.len ? end : at.len);
+            const int64_t hk = h / p.rep;
+            const int rows = (int)(p.P - p0 < DV ? p.P - p0 : DV);
+            const bool key = row < p.N;  // (row: a key here)
+            const float* const rec = a.rec + unit * (a.pieces - 1) * (DV * C) + row;
+            const T* const k = static_cast<const T*>(p.k) + b * p.k_b + hk * p.k_h + row;
+            const T* const q = static_cast<const T*>(p.q) + b * p.q_b + hk * p.q_h + row;
+            const float* const g = p.g + b * p.g_b + h * p.g_h;
+#pragma unroll 1
+            for (int j = 0; j < rows; ++j) {
+                const T* const v = static_cast<const T*>(p.v) + b * p.v_b + h * p.v_h + p0 + j;
+                int bad = INT_MAX;
+                for (int t = t0 + row; t < t1 && bad == INT_MAX; t += C)
+                    if (!(fabsf(to_f<T>(v[t * p.v_t])) < INFINITY)) bad = t;
+                bad = __reduce_min_sync(0xffffffffu, bad);
+                if (lane == 0) sm.first[w] = bad;
+                if (!sync()) return false;
+                bad = min(min(sm.first[0], sm.first[1]), min(sm.first[2], sm.first[3]));
+                if (!sync()) return false;
+                const int chunk = bad / C * C;
+                if (bad == INT_MAX || bad == chunk) continue;
+                float s = 0.0f;
+                if (p.s_in && key && piece == 0) s = p.s_in[b * p.si_b + h * p.si_h + (p0 + j) * p.si_p + row * p.si_n];
+                if (a.phase == 2)
+                    for (int i = 0; i < piece; ++i)
+                        s = fmaf(i == 0 ? 0.0f : exp2f((float)a.rec_g[unit * (a.pieces - 1) + i]), s,
+                                 rec[(int64_t)(i * DV + j) * C]);
+                auto token = [&](int t) {
+                    const float decay = g[t * p.g_t];
+                    s = fmaf(to_f<T>(v[t * p.v_t]), key ? to_f<T>(k[t * p.k_t]) : 0.0f,
+                             expf(decay > 0.0f ? 0.0f : decay) * s);
+                };
+#pragma unroll 8
+                for (int t = t0; t < chunk; ++t) token(t);
+#pragma unroll 1
+                for (int t = chunk; t < bad; ++t) {
+                    token(t);
+                    float sum = key ? s * to_f<T>(q[t * p.q_t]) : 0.0f;
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == 0) sm.part[w] = sum;
+                    if (!sync()) return false;
+                    if (row == 0)
+                        static_cast<T*>(p.out)[b * p.o_b + h * p.o_h + t * p.o_t + p0 + j] =
+                            from_f<T>(((sm.part[0] + sm.part[1]) + (sm.part[2] + sm.part[3])) * p.scale);
+                    if (!sync()) return false;
+                }
+            }
+            return true;
+        };
+        int i = 0;
+        while (start && i < n && values(i)) ++i;
+        if (outputs && n > 0 && i == n && wait(&sm.state_done, 0) && *(volatile int*)&sm.not_finite && repair()) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.repaired);
+        }
     }
     __syncthreads();
     tc_fence_after();

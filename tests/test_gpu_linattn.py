@@ -59,13 +59,13 @@ def bounds(q, k, v, g, s0, scale, lens, io, ref_out, chunk):
     return out, (f32 + (2.0 ** -22 if chunk else 0.0)) * ms
 
 
-def run(q, k, v, g, s0, scale=1.0, lens=None, io="f32", layout="token", workspace="auto"):
+def run(q, k, v, g, s0, scale=1.0, lens=None, io="f32", layout="token", workspace="auto", in_place=False):
     import torch
     from state_space_model_causal_b200 import LaunchInfo, binding, ssm_device_error, ssm_linear_attention_fwd
     put = token_major if layout == "token" else T
     tq, tk, tv = (put(a, io) for a in (q, k, v))
     st = T(s0, "f32") if s0 is not None else None
-    so = torch.full((v.shape[0], v.shape[1], v.shape[3], q.shape[3]), 7.0, device="cuda")
+    so = st if in_place else torch.full((v.shape[0], v.shape[1], v.shape[3], q.shape[3]), 7.0, device="cuda")
     out = torch.full_like(tv, 3.0)
     li = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
     info = LaunchInfo()
@@ -124,6 +124,44 @@ def test_padded_batch_with_garbage_behind_the_end(io):
     out, S, kern = run(q, k, v, g, s0, lens=lens, io=io)
     clean = [np.where(np.isfinite(a), a, 0.0) for a in (q, k, v, g)]
     check((*clean, s0), 1.0, lens, io, out, S, kern)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+def test_what_is_not_finite_reaches_no_earlier_token(io, in_place):
+    """Infinities and NaN among the values and keys of a sequence: the outputs before
+    their token, and the other columns and heads, are what they are without them."""
+    q, k, v, g, s0 = problem(1, 3, 3, 300, 64, 96, io, "token", seed=9)
+    bad_v, bad_k = v.copy(), k.copy()
+    bad_v[0, 0, 70, 5], bad_v[0, 0, 200, 66], bad_v[0, 1, 0, 0], bad_v[0, 1, 299, 95] = np.inf, np.nan, -np.inf, np.inf
+    bad_k[0, 1, 290, 3] = np.nan
+    clean = q, np.where(np.isfinite(bad_k), k, 0.0), np.where(np.isfinite(bad_v), v, 0.0), g, s0
+    reach, state_reach = np.zeros(v.shape, bool), np.zeros(s0.shape, bool)
+    reach[0, 0, 70:, 5] = reach[0, 0, 200:, 66] = reach[0, 1, :, 0] = reach[0, 1, 299:, 95] = reach[0, 1, 290:] = True
+    state_reach[0, 0, [5, 66]] = state_reach[0, 1, [0, 95]] = state_reach[0, 1, :, 3] = True
+    out, S, kern = run(q, bad_k, bad_v, g, s0, io=io, in_place=in_place)
+    assert not np.isfinite(out[reach]).any() and not np.isfinite(S[state_reach]).any()
+    ref_out, ref_S = ref.linear_attention(*clean[:4], 1.0, s0, None)
+    check(clean, 1.0, None, io, np.where(reach, ref_out, out), np.where(state_reach, ref_S, S), kern)
+
+
+@pytest.mark.parametrize("io", ["f16", "bf16"])
+def test_what_is_not_finite_in_pieces_of_a_long_sequence(io):
+    """As above where sequences are cut into pieces: in the first, in the others and in
+    a padded end."""
+    q, k, v, g, s0 = problem(2, 1, 1, 2500, 64, 64, io, "token", seed=10)
+    bad = v.copy()
+    bad[0, 0, 100, 3], bad[0, 0, 1200, 40], bad[0, 0, 2499, 63] = np.nan, np.inf, -np.inf
+    bad[1, 0, 2000, 5], bad[1, 0, 2101:] = np.inf, np.nan
+    lens = [2500, 2101]
+    reach, state_reach = np.zeros(v.shape, bool), np.zeros(s0.shape, bool)
+    reach[0, 0, 100:, 3] = reach[0, 0, 1200:, 40] = reach[0, 0, 2499:, 63] = reach[1, 0, 2000:2101, 5] = True
+    state_reach[0, 0, [3, 40, 63]] = state_reach[1, 0, 5] = True
+    clean = q, k, np.where(np.isfinite(bad), v, 0.0), g, s0
+    out, S, kern = run(q, k, bad, g, s0, io=io, lens=lens)
+    assert kern == "linattn_chunk" and not np.isfinite(out[reach]).any() and not np.isfinite(S[state_reach]).any()
+    ref_out, ref_S = ref.linear_attention(*clean[:4], 1.0, s0, lens)
+    check(clean, 1.0, lens, io, np.where(reach, ref_out, out), np.where(state_reach, ref_S, S), kern)
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16", "f16"])
