@@ -56,114 +56,132 @@ __device__ __forceinline__ float reduce_many(float (&v)[K], int lane) {
     return v[0];
 }
 
-// Prompt, any layout.  Bound by the latency of a token's chain (decay and FMA,
-// then the reduction, whose result nothing waits for): U tokens are loaded
-// while the U before them are computed, and their 4 U sums reduced together.
-template <typename T, int NE, int U, int kWarpRows>
+// Prompt, any layout.  A warp holds R rows of S in registers, a lane NE neighbouring
+// keys.  The CTA's threads bring the next stage of tokens (1024 numbers of k and of q, so 4 to
+// 32 tokens) into registers while its warps work on the last one from shared memory,
+// as float32; 4 tokens' sums are reduced together.
+constexpr int kStageNumbers = 1024;
+template <typename T, int NE, int R>
 __global__ void __launch_bounds__(kBlock) linattn_generic_kernel(const LinAttnProblem p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t nblk = (p.P + 4 * kWarpRows - 1) / (4 * kWarpRows);
+    constexpr int NP = 32 * NE, U = kStageNumbers / NP, ROWS = 4 * R;   // U: tokens per stage
+    constexpr int PER = kStageNumbers / kBlock, VPER = (U * ROWS + kBlock - 1) / kBlock;
+    __shared__ __align__(16) float ks[2][kStageNumbers], qs[2][kStageNumbers];
+    __shared__ __align__(16) float vs[2][U * ROWS];
+    __shared__ float2 gs[2][U];  // the decay's factor, and 1 if that is its distance from 1
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t nblk = (p.P + ROWS - 1) / ROWS;
     const int64_t unit = blockIdx.x / nblk;
     const int64_t b = unit / p.H, h = unit - b * p.H;
-    const int64_t p0 = ((blockIdx.x - unit * nblk) * 4 + (threadIdx.x >> 5)) * kWarpRows;
-    if (p0 >= p.P) return;
+    const int64_t c0 = (blockIdx.x - unit * nblk) * ROWS, p0 = c0 + warp * R;  // rows of the CTA, of the warp
     int64_t len = p.L;
     if (p.lens) {
         const int64_t n = p.lens[b * p.len_b];
         len = n < 0 ? 0 : (n < p.L ? n : p.L);
     }
-    float s[kWarpRows][NE];
+    auto key = [&](int i) { return NE <= 4 ? lane * NE + i : (i >> 2) * 128 + lane * 4 + (i & 3); };
+    float s[R][NE];
 #pragma unroll
-    for (int r = 0; r < kWarpRows; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int64_t n = lane + 32 * i;
-            s[r][i] = p.s_in && p0 + r < p.P && n < p.N
-                          ? p.s_in[b * p.si_b + h * p.si_h + (p0 + r) * p.si_p + n * p.si_n] : 0.0f;
-        }
-    const T* q = static_cast<const T*>(p.q) + b * p.q_b + (h / p.rep) * p.q_h;
-    const T* k = static_cast<const T*>(p.k) + b * p.k_b + (h / p.rep) * p.k_h;
-    const T* v = static_cast<const T*>(p.v) + b * p.v_b + h * p.v_h;
-    const float* g = p.g + b * p.g_b + h * p.g_h;
-    T* out = static_cast<T*>(p.out) + b * p.o_b + h * p.o_h;
+        for (int i = 0; i < NE; ++i)
+            s[r][i] = p.s_in && p0 + r < p.P && key(i) < p.N
+                          ? p.s_in[b * p.si_b + h * p.si_h + (p0 + r) * p.si_p + key(i) * p.si_n] : 0.0f;
+    T* const out = static_cast<T*>(p.out) + b * p.o_b + h * p.o_h;
 
-    float kn[U][NE], qn[U][NE], vn[U][kWarpRows], gn = 0.0f;  // gn: of token lane % U
+    // this thread's numbers of a stage: of k and q token u0 + j * du, key n0 (NP = 256: both halves in turn)
+    constexpr int kSplit = NP > kBlock ? 2 : 1;
+    constexpr int du = NP > kBlock ? 1 : kBlock / NP;
+    const int u0 = NP > kBlock ? 0 : threadIdx.x / NP, n0 = threadIdx.x % (NP > kBlock ? kBlock : NP);
+    const T* const q0 = static_cast<const T*>(p.q) + b * p.q_b + (h / p.rep) * p.q_h + n0 * p.q_n;
+    const T* const k0 = static_cast<const T*>(p.k) + b * p.k_b + (h / p.rep) * p.k_h + n0 * p.k_n;
+    const T* const v0 = static_cast<const T*>(p.v) + b * p.v_b + h * p.v_h;
+    const float* const g0 = p.g + b * p.g_b + h * p.g_h;
+    float kn[PER], qn[PER], vn[VPER], gn = 0.0f;
     auto load = [&](int64_t t0) {
-        gn = t0 + lane % U < len ? decay_log(g[(t0 + lane % U) * p.g_t]) : 0.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t t = t0 + u;
-            const bool on = t < len;
-#pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                const int64_t n = lane + 32 * i;
-                kn[u][i] = on && n < p.N ? to_f<T>(k[t * p.k_t + n * p.k_n]) : 0.0f;
-                qn[u][i] = on && n < p.N ? to_f<T>(q[t * p.q_t + n * p.q_n]) : 0.0f;
-            }
-#pragma unroll
-            for (int r = 0; r < kWarpRows; ++r)
-                vn[u][r] = on && p0 + r < p.P ? to_f<T>(v[t * p.v_t + (p0 + r) * p.v_p]) : 0.0f;
+        for (int j = 0; j < PER; ++j) {
+            const int64_t t = t0 + u0 + (j / kSplit) * du;
+            const int half = (j % kSplit) * kBlock;
+            const bool on = t < len && n0 + half < p.N;
+            kn[j] = on ? to_f<T>(k0[t * p.k_t + half * p.k_n]) : 0.0f;
+            qn[j] = on ? to_f<T>(q0[t * p.q_t + half * p.q_n]) : 0.0f;
         }
+#pragma unroll
+        for (int j = 0; j < VPER; ++j) {
+            const int e = threadIdx.x + j * kBlock, u = e / ROWS;
+            const int64_t t = t0 + u, row = c0 + e % ROWS;
+            vn[j] = u < U && t < len && row < p.P ? to_f<T>(v0[t * p.v_t + row * p.v_p]) : 0.0f;
+        }
+        if (threadIdx.x < U) gn = t0 + threadIdx.x < len ? decay_log(g0[(t0 + threadIdx.x) * p.g_t]) : 0.0f;
     };
     load(0);
-    for (int64_t t0 = 0; t0 < len; t0 += U) {
+    for (int64_t t0 = 0, buf = 0; t0 < len; t0 += U, buf ^= 1) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int at = (u0 + (j / kSplit) * du) * NP + n0 + (j % kSplit) * kBlock;
+            ks[buf][at] = kn[j];
+            qs[buf][at] = qn[j];
+        }
+#pragma unroll
+        for (int j = 0; j < VPER; ++j)
+            if (threadIdx.x + j * kBlock < U * ROWS) vs[buf][threadIdx.x + j * kBlock] = vn[j];
         // The decay is applied as S + (exp(g) - 1) S where it is above a half: the error of a
         // factor close to 1 would add up over the tokens that S remembers, that
         // of its distance from 1 does not.
-        float kc[U][NE], qc[U][NE], vc[U][kWarpRows], lam[U];
-        bool near1[U];
-        const bool near = gn > -0.6931f;
-        const float decay = near ? expm1f(gn) : expf(gn);
-        const uint32_t nears = __ballot_sync(0xffffffffu, near);
+        // Tokens past the end have v = 0 and a factor of 1.
+        if (threadIdx.x < U)
+            gs[buf][threadIdx.x] = t0 + threadIdx.x >= len ? make_float2(1.0f, 0.0f)
+                                   : gn > -0.6931f ? make_float2(expm1f(gn), 1.0f) : make_float2(expf(gn), 0.0f);
+        __syncthreads();  // (the other buffer is written after the next one)
+        if (t0 + U < len) load(t0 + U);
+        const int count = (int)(len - t0 < U ? len - t0 : U);
+        for (int u = 0; u < count; u += 4) {
+            float sum[4 * R];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            near1[u] = nears >> u & 1;
-            lam[u] = __shfl_sync(0xffffffffu, decay, u);
+            for (int x = 0; x < 4; ++x) {
+                float kf[NE], qf[NE], vf[R];
+                const float2 lam = gs[buf][u + x];
+                const bool near1 = lam.y != 0.0f;
 #pragma unroll
-            for (int i = 0; i < NE; ++i) kc[u][i] = kn[u][i], qc[u][i] = qn[u][i];
+                for (int i = 0; i < NE; ++i) {
+                    kf[i] = ks[buf][(u + x) * NP + key(i)];
+                    qf[i] = qs[buf][(u + x) * NP + key(i)];
+                }
 #pragma unroll
-            for (int r = 0; r < kWarpRows; ++r) vc[u][r] = vn[u][r];
-        }
-        load(t0 + U);
-        float sum[U * kWarpRows];
+                for (int r = 0; r < R; ++r) vf[r] = vs[buf][(u + x) * ROWS + warp * R + r];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int r = 0; r < kWarpRows; ++r) {
-                float acc = 0.0f;
-                if (t0 + u < len) {  // past the end: the state stays
+                for (int r = 0; r < R; ++r) {
+                    float acc = 0.0f;
 #pragma unroll
                     for (int i = 0; i < NE; ++i) {
-                        s[r][i] = fmaf(lam[u], s[r][i], fmaf(vc[u][r], kc[u][i], near1[u] ? s[r][i] : 0.0f));
-                        acc = fmaf(s[r][i], qc[u][i], acc);
+                        s[r][i] = fmaf(lam.x, s[r][i], fmaf(vf[r], kf[i], near1 ? s[r][i] : 0.0f));
+                        acc = fmaf(s[r][i], qf[i], acc);
                     }
+                    sum[x * R + r] = acc;
                 }
-                sum[u * kWarpRows + r] = acc;
             }
-        constexpr int K = U * kWarpRows;  // 8 or 16 sums
-        const float o = reduce_many<K>(sum, lane);
-        const int idx = lane / (32 / K);
-        const int64_t t = t0 + idx / kWarpRows, row = p0 + idx % kWarpRows;
-        if (lane % (32 / K) == 0 && t < len && row < p.P)
-            out[t * p.o_t + row * p.o_p] = from_f<T>(o * p.scale);
+            const float o = reduce_many<4 * R>(sum, lane);
+            constexpr int share = 32 / (4 * R);  // lanes that hold the same sum
+            const int idx = lane / share;
+            const int64_t t = t0 + u + idx / R, row = p0 + idx % R;
+            if (lane % share == 0 && t < len && row < p.P) out[t * p.o_t + row * p.o_p] = from_f<T>(o * p.scale);
+        }
     }
     if (!p.s_out) return;
 #pragma unroll
-    for (int r = 0; r < kWarpRows; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int64_t n = lane + 32 * i;
-            if (p0 + r < p.P && n < p.N)
-                p.s_out[b * p.so_b + h * p.so_h + (p0 + r) * p.so_p + n * p.so_n] = s[r][i];
-        }
+        for (int i = 0; i < NE; ++i)
+            if (p0 + r < p.P && key(i) < p.N)
+                p.s_out[b * p.so_b + h * p.so_h + (p0 + r) * p.so_p + key(i) * p.so_n] = s[r][i];
 }
 
 template <typename T, int R>
 cudaError_t generic_t(const LinAttnProblem& p, int grid, cudaStream_t s) {
-    if (p.N <= 32) linattn_generic_kernel<T, 1, 4, R><<<grid, kBlock, 0, s>>>(p);
-    else if (p.N <= 64) linattn_generic_kernel<T, 2, 4, R><<<grid, kBlock, 0, s>>>(p);
-    else if (p.N <= 128) linattn_generic_kernel<T, 4, 4, R><<<grid, kBlock, 0, s>>>(p);
-    else linattn_generic_kernel<T, 8, 2, R><<<grid, kBlock, 0, s>>>(p);
+    if (p.N <= 32) linattn_generic_kernel<T, 1, R><<<grid, kBlock, 0, s>>>(p);
+    else if (p.N <= 64) linattn_generic_kernel<T, 2, R><<<grid, kBlock, 0, s>>>(p);
+    else if (p.N <= 128) linattn_generic_kernel<T, 4, R><<<grid, kBlock, 0, s>>>(p);
+    else linattn_generic_kernel<T, 8, R><<<grid, kBlock, 0, s>>>(p);
     return cudaGetLastError();
 }
 
