@@ -587,6 +587,23 @@ def ssm_gated_conv1d_fwd(x, b_gate, c_gate, weight, bias=None, conv_state=None, 
     return out
 
 
+def _empty(shape, dtype, dev, stream):
+    """An output allocated on the stream that writes it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(dev, stream), device=dev)):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _empty_like(t, stream):
+    import torch
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(t.device, stream), device=t.device)):
+        return torch.empty_like(t)
+
+
 def _call_with_workspace(fn, size_fn, what, args, tensors, stream, workspace, optional):
     """Call an entry point whose workspace holds nothing between calls: "auto"
     allocates one for this call on its stream (the caching allocator reuses
@@ -603,11 +620,7 @@ def _call_with_workspace(fn, size_fn, what, args, tensors, stream, workspace, op
             need = ctypes.c_uint64(0)
             _check(size_fn(ctypes.byref(args), ctypes.byref(need)), what)
             if need.value:
-                if stream is None:
-                    ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-                else:
-                    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-                        ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+                ws = _empty(need.value, torch.uint8, dev, stream)
         elif workspace is not None:
             ws = workspace
         elif not optional:
@@ -628,9 +641,8 @@ def ssm_linear_attention_fwd(q, k, v, log_decay, scale=1.0, state=None, state_ou
     or (B, H, L) float32; state (B, H, P, N) float32, read as S_0 and updated
     in place, or only read when state_out is given; seq_lens (B) int32.
     Without ``out``, the output takes v's order of dimensions.  Returns out."""
-    import torch
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty_like(v, stream)
     tensors = (q, k, v, log_decay, state, state_out, seq_lens, out)
     a = _make_args(LinAttnArgs, _LINATTN, tensors, info)
     a.scale = scale
@@ -650,9 +662,8 @@ def ssm_linear_attention_update(state, q, k, v, log_decay, scale=1.0, state_batc
     state (S, H, P, N); q, k (B, Hk, N); v (B, H, P); log_decay (H) or (B, H)
     float32; state_batch_indices (B) int32 slots.  The state is updated in
     place, or written to state_out and only read.  Returns out (B, H, P)."""
-    import torch
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty_like(v, stream)
     tensors = (state, q, k, v, log_decay, state_batch_indices, state_out, out)
     a = _make_args(LinAttnUpdateArgs, _LINATTN_UPDATE, tensors, info)
     a.scale = scale
@@ -672,9 +683,8 @@ def ssm_paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, scale
     block_table (B, M) int32; seq_lens (B) int32; scale: 1 / sqrt(D) unless
     given; weights (B, Hkv, T) float32, to which the attention weights are
     added (in place, or into weights_out).  Returns out (B, Hq, D)."""
-    import torch
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     tensors = (q, k_cache, v_cache, block_table, seq_lens, weights, weights_out, lse, out)
     a = _make_args(PagedAttentionArgs, _PAGED, tensors, info)
     a.scale = q.shape[-1] ** -0.5 if scale is None else scale
@@ -697,21 +707,13 @@ def ssm_kv_cache_evict(k_cache, v_cache, weights, block_table, seq_lens, new_blo
     (new_seq_lens (B) int32, kept (B, Hkv, keep) int32: former positions,
     new_weights (B, Hkv, keep) float32)."""
     import torch
-    B, Hkv = block_table.shape[0], k_cache.shape[2]
-
-    def make(shape, dtype):
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=k_cache.device)
-        with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(k_cache.device, stream),
-                                                         device=k_cache.device)):
-            return torch.empty(shape, dtype=dtype, device=k_cache.device)
-
+    B, Hkv, dev = block_table.shape[0], k_cache.shape[2], k_cache.device
     if new_weights is None:
-        new_weights = make((B, Hkv, keep), torch.float32)
+        new_weights = _empty((B, Hkv, keep), torch.float32, dev, stream)
     if new_seq_lens is None:
-        new_seq_lens = make((B,), torch.int32)
+        new_seq_lens = _empty((B,), torch.int32, dev, stream)
     if kept is None:
-        kept = make((B, Hkv, keep), torch.int32)
+        kept = _empty((B, Hkv, keep), torch.int32, dev, stream)
     tensors = (k_cache, v_cache, weights, block_table, seq_lens, new_block_table, new_weights, new_seq_lens, kept)
     a = _make_args(KvEvictArgs, _EVICT, tensors, info)
     a.keep, a.recent = keep, recent

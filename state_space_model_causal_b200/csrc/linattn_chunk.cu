@@ -228,7 +228,8 @@ __device__ __forceinline__ void fewer_registers() {
 // Code size: 20 warps run a dozen different loops, each once per chunk.  Unrolled
 // throughout, they did not fit the instruction caches, and warps waited for
 // instructions more than for anything else (10 of 26 stalled warps per issue; 237 us
-// for 4 x 2048 tokens of 32 heads of 128).  So loops over blocks of 32 columns stay loops.
+// for 4 x 2048 tokens of 32 heads of 128).  So loops over blocks of 32 columns, and the one that
+// makes V~, stay loops: 108 us (with V~ unrolled by 4 115, wholly 133).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
 linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -746,7 +747,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             if (i > 0 && !wait(&sm.kv_full, (i - 1) & 1)) return false;
             if (HT::kScaled && row == 0) sm.v_lift[i & 1] = lift;
             const u64 factor2 = pk(factor, factor);
-#pragma unroll 2
+#pragma unroll 1
             for (int j = 0; j < 8; ++j) {
                 const int at = (j ^ (row & 7)) << 4;
                 float f[8];

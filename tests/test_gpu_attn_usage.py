@@ -80,6 +80,30 @@ def test_on_another_stream(how):
     assert np.abs(to_np(out) - ref_out).max() < 0.03 * np.abs(ref_out).max()
 
 
+def test_outputs_are_allocated_on_the_stream_that_writes_them():
+    """With a stream argument: memory that the current stream freed a moment ago may still
+    be read there."""
+    import torch
+    from state_space_model_causal_b200 import (ssm_kv_cache_evict, ssm_linear_attention_fwd,
+                                               ssm_linear_attention_update, ssm_paged_attention_decode)
+    _, (q, k, v, g, s0) = prompt_inputs()
+    (pq, pk, pv, table, lens), _ = paged_inputs(1)
+    w = torch.rand(3, 2, 640, device="cuda")
+    new = table.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [ssm_linear_attention_fwd(q, k, v, g, state=s0, stream=side),
+            ssm_linear_attention_update(s0, q[:, :, 0].contiguous(), k[:, :, 0].contiguous(), v[:, :, 0].contiguous(),
+                                        g[:, :, 0].contiguous(), stream=side),
+            ssm_paged_attention_decode(pq, pk, pv, table, lens, stream=side),
+            *ssm_kv_cache_evict(pk, pv, w, table, lens * 0, new, keep=5, recent=2, stream=side)]
+    torch.cuda.synchronize()
+    segments = torch.cuda.memory_snapshot()
+    for o in outs:
+        home = [x for x in segments if x["address"] <= o.data_ptr() < x["address"] + x["total_size"]]
+        assert [x["stream"] for x in home] == [side.cuda_stream]
+
+
 def test_two_calls_at_once():
     """Prompts and decode steps on two streams at the same time."""
     import torch
