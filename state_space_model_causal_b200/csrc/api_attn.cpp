@@ -355,7 +355,7 @@ ssm_status paged_impl(const ssm_paged_attention_args* a, cudaStream_t stream, ui
     p.page_shift = -1;
     for (int i = 0; i < 31; ++i)
         if (page == (int64_t)1 << i) p.page_shift = i;
-    p.G = Hq / Hkv; p.cap = cap; p.io_dt = io;
+    p.G = Hq / Hkv; p.cap = cap; p.ws_cap = (cap + 3) / 4 * 4; p.io_dt = io;
     p.hpb = paged_heads_per_cta(kernel, p.G);
     p.hblocks = (int)((p.G + p.hpb - 1) / p.hpb);
     if (Hkv * p.hblocks > 65535 || B > (int64_t)INT32_MAX / Hq ||
@@ -369,7 +369,7 @@ ssm_status paged_impl(const ssm_paged_attention_args* a, cudaStream_t stream, ui
     const uint64_t parts = (uint64_t)p.workers * heads * 2 * p.hpb;
     const uint64_t at_ml = round256(parts * D * 4), at_lse = at_ml + round256(parts * 8);
     const uint64_t at_s = at_lse + (has_w ? round256((uint64_t)B * Hq * 4) : 0);
-    const uint64_t need = at_s + (has_w ? round256((uint64_t)B * Hq * cap * 4) : 0);
+    const uint64_t need = at_s + (has_w ? round256((uint64_t)B * Hq * p.ws_cap * 4) : 0);
     if (ws_query) {
         *ws_query = need;
         return SSM_OK;

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kBlock) paged_generic_kernel(const PagedProble
 #pragma unroll
                     for (int g = 0; g < HPB; ++g)
                         if (lane == u * HPB + g && t + u < t1 && g < heads)
-                            p.ws_s[(b * p.Hq + hk * p.G + (int64_t)hblk * HPB + g) * p.cap + t + u] = x[u][g];
+                            p.ws_s[(b * p.Hq + hk * p.G + (int64_t)hblk * HPB + g) * p.ws_cap + t + u] = x[u][g];
             }
 #pragma unroll
             for (int g = 0; g < HPB; ++g) {
@@ -501,12 +501,10 @@ __global__ void __launch_bounds__(kBlock, WIDE ? 2 : 3) paged_mma_kernel(const P
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j] = on[j] ? s[j >> 1][2 * w + (j & 1)] * p.scale_log2 : kNegInf;
                     if (p.w && r + 8 * w < heads) {
-                        float* ws = p.ws_s + (b * p.Hq + hq0 + r + 8 * w) * p.cap;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int tk = t + 2 * c + (j & 1) + 8 * (j >> 1);
-                            if (tk < t1) ws[tk] = x[j];
-                        }
+                        // pairs of tokens (behind the end of the sequence the second is not read)
+                        float* ws = p.ws_s + (b * p.Hq + hq0 + r + 8 * w) * p.ws_cap + t + 2 * c;
+                        if (t + 2 * c < t1) *reinterpret_cast<float2*>(ws) = make_float2(x[0], x[1]);
+                        if (t + 2 * c + 8 < t1) *reinterpret_cast<float2*>(ws + 8) = make_float2(x[2], x[3]);
                     }
                     float mx = max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
                     mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -681,24 +679,32 @@ __global__ void __launch_bounds__(kBlock) paged_join_kernel(const PagedProblem p
 }
 
 // Accumulated weights: the scores of the first kernel against the joined
-// denominators.  A thread takes one token of one key-value head.
-constexpr int kWeightTokens = 512;  // tokens per CTA
+// denominators.  A thread takes 4 neighbouring tokens of one key-value head.
+constexpr int kWeightTokens = 4 * kBlock;  // tokens per CTA
 __global__ void __launch_bounds__(kBlock) paged_weights_kernel(const PagedProblem p) {
     const int64_t blocks = (p.cap + kWeightTokens - 1) / kWeightTokens;
     const int64_t row = blockIdx.x / blocks, b = row / p.Hkv, hk = row - b * p.Hkv;
     const int64_t len = seq_len(p, b);
-    const int64_t t0 = (blockIdx.x - row * blocks) * kWeightTokens;
-    const int64_t t1 = t0 + kWeightTokens < len ? t0 + kWeightTokens : len;
+    const int64_t t = (blockIdx.x - row * blocks) * kWeightTokens + 4 * threadIdx.x;
+    const float* const w = p.w + b * p.w_b + hk * p.w_h;
+    float* const w_out = p.w_out + b * p.wo_b + hk * p.wo_h;
+    float sum[4] = {}, old[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) old[j] = t + j < len ? w[(t + j) * p.w_t] : 0.0f;  // (not the last kernel's)
     wait_for_previous_kernel();
-    for (int64_t t = t0 + threadIdx.x; t < t1; t += kBlock) {
-        float sum = 0.0f;
-        for (int64_t g = 0; g < p.G; ++g) {
-            const int64_t hq = b * p.Hq + hk * p.G + g;
-            const float lse2 = p.ws_lse2[hq], x = p.ws_s[hq * p.cap + t];
-            sum += lse2 == kNegInf || x == kNegInf ? 0.0f : exp2f(x - lse2);
-        }
-        p.w_out[b * p.wo_b + hk * p.wo_h + t * p.wo_t] = p.w[b * p.w_b + hk * p.w_h + t * p.w_t] + sum;
+    if (t >= len) return;
+#pragma unroll 4
+    for (int64_t g = 0; g < p.G; ++g) {
+        const int64_t hq = b * p.Hq + hk * p.G + g;
+        const float lse2 = p.ws_lse2[hq];
+        const float4 x4 = *reinterpret_cast<const float4*>(p.ws_s + hq * p.ws_cap + t);
+        const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] += lse2 == kNegInf || x[j] == kNegInf ? 0.0f : exp2f(x[j] - lse2);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (t + j < len) w_out[(t + j) * p.wo_t] = old[j] + sum[j];
 }
 
 // a launch that may start before the stream's last kernel has finished

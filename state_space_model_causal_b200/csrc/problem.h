@@ -278,7 +278,8 @@ struct PagedProblem {
     float* ws_o;          // [worker][hkv][hblock][2][hpb][D]
     float2* ws_ml;        // [worker][hkv][hblock][2][hpb]: maximum (log2), sum
     float* ws_lse2;       // [b][hq]: log2 of the softmax's denominator (with weights)
-    float* ws_s;          // [b][hq][cap]: scores in log2 (with weights)
+    float* ws_s;          // [b][hq][ws_cap]: scores in log2 (with weights)
+    int64_t ws_cap;       // cap, rounded up to a multiple of 4
 };
 
 struct BoundedWaits {
