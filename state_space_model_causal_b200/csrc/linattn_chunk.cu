@@ -738,6 +738,14 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 #pragma unroll
                     for (int u = 0; u < 8; ++u) mx = fmaxf(mx, fabsf(f[u]));
                 }
+                if (mx == INFINITY) {  // (a NaN does not count as it is)
+                    mx = 0.0f;
+#pragma unroll 1
+                    for (int j = 0; j < DV; ++j) {
+                        const float f = fabsf(to_f<T>(reinterpret_cast<const T*>(vrow)[j]));
+                        if (f < INFINITY) mx = fmaxf(mx, f);
+                    }
+                }
                 uint32_t top;
                 if (!group_max(mx * weight, 1, i, top)) return false;
                 lift = lift_of(top);

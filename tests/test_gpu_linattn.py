@@ -145,6 +145,22 @@ def test_what_is_not_finite_reaches_no_earlier_token(io, in_place):
     check(clean, 1.0, None, io, np.where(reach, ref_out, out), np.where(state_reach, ref_S, S), kern)
 
 
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
+def test_small_values_beside_one_that_is_not_finite(bad):
+    """float16 values far below 1, which its two numbers hold by a common power of two:
+    what is not finite has no part in that."""
+    q, k, v, g, s0 = problem(1, 1, 1, 40, 64, 64, "f16", "token", seed=11, state=False)
+    v = gen.round_to(v * 1e-4, "f16")
+    bad_v, clean = v.copy(), v.copy()
+    bad_v[0, 0, 30, 7], clean[0, 0, 30, 7] = bad, 0.0
+    reach, state_reach = np.zeros(v.shape, np.bool_), np.zeros((1, 1, 64, 64), np.bool_)
+    reach[0, 0, 30:, 7] = state_reach[0, 0, 7] = True
+    out, S, kern = run(q, k, bad_v, g, s0, io="f16")
+    assert kern == "linattn_chunk" and not np.isfinite(out[reach]).any() and not np.isfinite(S[state_reach]).any()
+    ref_out, ref_S = ref.linear_attention(q, k, clean, g, 1.0, s0, None)
+    check((q, k, clean, g, s0), 1.0, None, "f16", np.where(reach, ref_out, out), np.where(state_reach, ref_S, S), kern)
+
+
 @pytest.mark.parametrize("io", ["f16", "bf16"])
 def test_what_is_not_finite_in_pieces_of_a_long_sequence(io):
     """As above where sequences are cut into pieces: in the first, in the others and in
