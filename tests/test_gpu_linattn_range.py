@@ -1,0 +1,71 @@
+"""Linear attention where the numbers are far apart: decays, scores, states and
+values whose sizes differ by tens of powers of two, and what is not finite.
+
+Tolerances: those of test_gpu_linattn, and for float16 prompts what a common
+power of two leaves of the small numbers beside a large one.  A number held in
+float16 under a scale that brings the largest to 2^13 or more is off by at most half a
+subnormal step, 2^-25, that is 2^-38 of the largest:
+
+* a score: 2^-38 of the largest |q_t . k_s| of its row, times |v_s|;
+* the copy of the state that queries read: 2^-38 of the largest |S| of its
+  64 values, times |q|, times the scale.
+"""
+import numpy as np
+import pytest
+
+from oracle import attention as ref
+from state_space_model_causal_b200 import inputs as gen
+from tests.test_gpu_linattn import bounds, problem, run
+
+pytestmark = pytest.mark.gpu
+
+
+def common_scale(q, k, v, s0, scale):
+    """The float16 terms above, for every output (B, H, L, P)."""
+    rep = v.shape[1] // q.shape[1]
+    q, k, v = np.repeat(np.abs(q), rep, 1), np.repeat(np.abs(k), rep, 1), np.abs(v)
+    row = np.maximum.accumulate(np.einsum("bhtn,bhsn->bhts", q, k), -1)
+    top = np.einsum("bhtt->bht", row)  # over s <= t
+    S = np.einsum("bhsp,bhsn->bhpn", v, k) + (0.0 if s0 is None else np.abs(s0))
+    most = S.max((2, 3))
+    return abs(scale) * 2.0 ** -38 * (top[..., None] * v.cumsum(2) + most[:, :, None, None] * q.sum(-1)[..., None])
+
+
+def check(args, got, scale, io, kernel, skip_out=None, skip_state=None, lens=None):
+    """Against the definition; skip: a mask of elements that are not compared here."""
+    q, k, v, g, s0 = args
+    out, S = ref.linear_attention(q, k, v, g, scale, s0, lens)
+    chunk = kernel == "linattn_chunk"
+    bo, bs = bounds(q, k, v, g, s0, scale, lens, io, out, chunk)
+    if chunk and io == "f16":
+        bo = bo + common_scale(q, k, v, s0, scale)
+    for what, a, b, bound, skip in (("out", got[0], out, bo, skip_out), ("state", got[1], S, bs, skip_state)):
+        on = np.ones(a.shape, bool) if skip is None else ~skip
+        assert np.isfinite(a[on]).all(), f"{what}: {(~np.isfinite(a[on])).sum()} not finite"
+        err = np.abs(a - b)[on] / (bound[on] + 1e-300)
+        assert err.max() <= 1.0, f"{what}: {(err > 1).sum()} of {err.size} off, worst {err.max():.3g} bounds"
+
+
+# Over 32 tokens these decay by 2^45 to 2^103: on both sides of the border to the form with
+# an exponential per element.
+DECAYS = [-1.0, -1.35, -1.6, -2.0, -2.2, -2.3, "one"]
+
+
+def decaying(log_decay, shape):
+    g = np.full(shape, log_decay if log_decay != "one" else -0.01)
+    if log_decay == "one":  # one token of a block forgets nearly everything, another a good deal
+        g[..., 17], g[..., 40] = -65.0, -45.0
+    return gen.round_to(g, "f32")
+
+
+@pytest.mark.parametrize("log_decay", DECAYS)
+@pytest.mark.parametrize("small", [0, 7, 10, 14])
+def test_float16_scores_below_one_under_strong_decay(log_decay, small):
+    """q and k of 2^-small: scores of about 2^(3 - 2 small), put right by the scale."""
+    q, k, v, _, s0 = problem(1, 2, 2, 160, 64, 64, "f16", "token", seed=71)
+    q, k = gen.round_to(q * 2.0 ** -small, "f16"), gen.round_to(k * 8 * 2.0 ** -small, "f16")
+    g, scale = decaying(log_decay, (1, 2, 160)), 2.0 ** (2 * small - 3)
+    s0 = s0 * 2.0 ** -small
+    out, S, kern = run(q, k, v, g, s0, scale=scale, io="f16")
+    assert kern == "linattn_chunk"
+    check((q, k, v, g, s0), (out, S), scale, "f16", kern)
