@@ -545,8 +545,9 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                     for (int j = 0; j < 32; j += 4) {
                         const float4 c4 = *reinterpret_cast<const float4*>(&sm.column[s][g * 32 + j]);
                         float x0, x1, x2, x3;
-                        upk(fmul2(f2, fmul2(pk(c4.x, c4.y), pk(__uint_as_float(r[j]), __uint_as_float(r[j + 1])))), x0, x1);
-                        upk(fmul2(f2, fmul2(pk(c4.z, c4.w), pk(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])))), x2, x3);
+                        // (the two factors first: a column's, 2^-100 or so, would take a small score out of range)
+                        upk(fmul2(fmul2(f2, pk(c4.x, c4.y)), pk(__uint_as_float(r[j]), __uint_as_float(r[j + 1]))), x0, x1);
+                        upk(fmul2(fmul2(f2, pk(c4.z, c4.w)), pk(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]))), x2, x3);
                         r[j] = __float_as_uint(x0);
                         r[j + 1] = __float_as_uint(x1);
                         r[j + 2] = __float_as_uint(x2);

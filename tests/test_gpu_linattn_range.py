@@ -69,3 +69,16 @@ def test_float16_scores_below_one_under_strong_decay(log_decay, small):
     out, S, kern = run(q, k, v, g, s0, scale=scale, io="f16")
     assert kern == "linattn_chunk"
     check((q, k, v, g, s0), (out, S), scale, "f16", kern)
+
+
+@pytest.mark.parametrize("log_decay", DECAYS)
+@pytest.mark.parametrize("small", [16, 30])
+def test_bfloat16_scores_far_below_one_under_strong_decay(log_decay, small):
+    """As above in bfloat16, whose scores can be as small as float32's."""
+    q, k, v, _, s0 = problem(1, 2, 2, 160, 64, 64, "bf16", "token", seed=72)
+    q, k = q * 2.0 ** -small, k * 8 * 2.0 ** -small
+    g, scale = decaying(log_decay, (1, 2, 160)), 2.0 ** (2 * small - 3)
+    s0 = s0 * 2.0 ** -small
+    out, S, kern = run(q, k, v, g, s0, scale=scale, io="bf16")
+    assert kern == "linattn_chunk"
+    check((q, k, v, g, s0), (out, S), scale, "bf16", kern)
