@@ -541,7 +541,8 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  * adds to it enters as a sum of 16-bit numbers (two for float16, three for
  * bfloat16), which loses at most 2^-22 of it.  An infinity counts as a NaN there:
  * one in v makes its column of the outputs from its token on, and of the state, NaN,
- * one in k every output from its token on.
+ * one in k every output from its token on, one in the initial state its column of the outputs.
+ * Other columns do not depend on it.
  *
  * The workspace holds the end states of the pieces that few long sequences
  * are cut into: ssm_linear_attention_workspace_size() returns its size in bytes

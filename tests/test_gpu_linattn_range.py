@@ -82,3 +82,22 @@ def test_bfloat16_scores_far_below_one_under_strong_decay(log_decay, small):
     out, S, kern = run(q, k, v, g, s0, scale=scale, io="bf16")
     assert kern == "linattn_chunk"
     check((q, k, v, g, s0), (out, S), scale, "bf16", kern)
+
+
+@pytest.mark.parametrize("size", [20, -20])
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("L", [40, 300])
+def test_initial_state_with_one_number_that_is_not_finite(L, bad, size):
+    """float16: the other value channels keep their common scale, for states above float16's
+    largest number and for states among its subnormals."""
+    q, k, v, g, s0 = problem(1, 2, 1, L, 64, 64, "f16", "token", seed=73)
+    s0, scale = s0 * 2.0 ** size, 2.0 ** -size
+    v = gen.round_to(v * 2.0 ** min(size, 0), "f16")
+    clean, bad_s0 = s0.copy(), s0.copy()
+    bad_s0[0, 0, 5, 3], clean[0, 0, 5, 3] = bad, 0.0
+    skip_out, skip_state = np.zeros(v.shape, bool), np.zeros(s0.shape, bool)
+    skip_out[0, 0, :, 5] = skip_state[0, 0, 5, 3] = True
+    out, S, kern = run(q, k, v, g, bad_s0, scale=scale, io="f16")
+    assert kern == "linattn_chunk"
+    assert not np.isfinite(out[skip_out]).any() and not np.isfinite(S[skip_state]).any()
+    check((q, k, v, g, clean), (out, S), scale, "f16", kern, skip_out, skip_state)
