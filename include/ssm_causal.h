@@ -535,11 +535,15 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  * either exactly `state` or does not overlap it.
  *
  * The chunk kernel's products are of 16-bit factors, summed in float32.  The
- * masked scores are rounded to q's dtype once (float16 with a power of two
- * taken out of every row, so that they cannot overflow), and so is the copy of the
- * state that queries read.  The state itself is held in float32; what a token
- * adds to it enters as a sum of 16-bit numbers (two for float16, three for
- * bfloat16), which loses at most 2^-22 of it.  An infinity counts as a NaN there:
+ * masked scores are rounded to q's dtype once, and so is the copy of the state
+ * that queries read.  In float16 a power of two is taken out of both, so that
+ * they cannot overflow (one for the scores of a token, one for 64 value
+ * channels of the state); a number that is small beside the largest one loses
+ * 2^-38 of that instead of 2^-11 of itself, if that is more.  The state itself
+ * is held in float32; what a token adds to it enters as a sum of 16-bit
+ * numbers (two for float16, three for bfloat16), which loses at most 2^-22 of
+ * it -- in float16, where 64 value channels of a chunk share a power of two,
+ * 2^-49 of their largest if that is more.  An infinity counts as a NaN there:
  * one in v makes its column of the outputs from its token on, and of the state, NaN,
  * one in k every output from its token on, one in the initial state its column of the outputs.
  * Other columns do not depend on it.

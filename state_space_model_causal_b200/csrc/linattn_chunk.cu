@@ -32,8 +32,8 @@
 //
 // Precision.  Accumulators and S are float32.  V~ is given to the tensor cores as
 // several 16-bit numbers, each holding what rounding those before it left over (three
-// for bf16: 24 bits of significand, two for f16: 22), because the state is a float32 result and
-// remembers for long.  The scores, and the copy of S that Q S reads, are
+// for bf16: 24 bits of significand, two for f16: 22, down to 2^-28 of the chunk's largest), because
+// the state is a float32 result and remembers for long.  The scores, and the copy of S that Q S reads, are
 // rounded once, as the output will be.  For f16, whose range is small, a power of two is taken out of every row of
 // scores, of V~ and of S, and put back in float32: it costs three maxima.
 //
@@ -163,7 +163,9 @@ __device__ __forceinline__ int lift_of(uint32_t exponent) {
 __device__ __forceinline__ uint32_t exponent_of(float v) { return __float_as_uint(v) >> 23 & 255u; }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// 16-bit numbers that add up to a value, for a pair
+// 16-bit numbers that add up to a value, for a pair; f16: the second 2^11 times as large, so that
+// it does not fall among the subnormals 2^11 before the first does
+constexpr float kSecond = 2048.0f;
 template <typename T>
 __device__ __forceinline__ void split2(u64 f, uint32_t (&part)[Half16<T>::kParts]) {
 #pragma unroll
@@ -173,6 +175,7 @@ __device__ __forceinline__ void split2(u64 f, uint32_t (&part)[Half16<T>::kParts
         part[i] = Half16<T>::two(x, y);
         const float2 back = Half16<T>::back(part[i]);
         f = fsub2(f, pk(back.x, back.y));
+        if (Half16<T>::kScaled) f = fmul2(f, pk(kSecond, kSecond));
     }
 }
 
@@ -682,9 +685,12 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
                     u64 add = pk(__uint_as_float(y[j]), __uint_as_float(y[j + 1]));
-                    if (HT::kParts == 3) add = fadd2(add, pk(__uint_as_float(z[j]), __uint_as_float(z[j + 1])));
-                    add = fadd2(add, pk(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
-                    if (HT::kScaled) add = fmul2(add, lift2);
+                    const u64 first = pk(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                    if (HT::kScaled) {
+                        add = fmul2(ffma2(add, pk(1.0f / kSecond, 1.0f / kSecond), first), lift2);
+                    } else {
+                        add = fadd2(fadd2(add, pk(__uint_as_float(z[j]), __uint_as_float(z[j + 1]))), first);
+                    }
                     const u64 s2 = pk(S[g + j], S[g + j + 1]);
                     u64 to = ffma2(f2, s2, add);
                     if (near1) to = fadd2(to, s2);

@@ -101,3 +101,22 @@ def test_initial_state_with_one_number_that_is_not_finite(L, bad, size):
     assert kern == "linattn_chunk"
     assert not np.isfinite(out[skip_out]).any() and not np.isfinite(S[skip_state]).any()
     check((q, k, v, g, clean), (out, S), scale, "f16", kern, skip_out, skip_state)
+
+
+@pytest.mark.parametrize("io", ["f16", "bf16"])
+@pytest.mark.parametrize("L", [5, 200])
+def test_value_channels_far_apart_in_size(io, L):
+    """Channels of 2^-16 to 2^12 beside one another: the state of each to the accuracy of its
+    own size (2^-22, and 2^-49 of the largest value in float16, see the header)."""
+    q, k, v, g, _ = problem(1, 2, 2, L, 64, 64, io, "token", seed=74, state=False)
+    v = gen.round_to(np.clip(v, -4, 4) * 2.0 ** (4.0 * (np.arange(64) % 8) - 16), io)
+    out, S, kern = run(q, k, v, g, None, io=io)
+    assert kern == "linattn_chunk"
+    _, ref_S = ref.linear_attention(q, k, v, g)
+    _, own = bounds(q, k, v, g, None, 1.0, None, io, np.zeros_like(v), True)
+    largest = np.abs(v).max((2, 3))[:, :, None, None] * np.abs(k).sum(2)[:, :, None, :]
+    err = np.abs(S - ref_S) / (own + 2.0 ** -49 * largest)
+    assert err.max() <= 1.0, f"worst {err.max():.3g} bounds, by channel size {err.max((0, 1, 3))[:8].round(2)}"
+    want, _ = ref.linear_attention(q, k, v, g)
+    bound, _ = bounds(q, k, v, g, None, 1.0, None, io, want, True)
+    assert (np.abs(out - want) <= bound + (common_scale(q, k, v, None, 1.0) if io == "f16" else 0.0)).all()
