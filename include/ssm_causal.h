@@ -546,7 +546,8 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  * 2^-49 of their largest if that is more.  An infinity counts as a NaN there:
  * one in v makes its column of the outputs from its token on, and of the state, NaN,
  * one in k every output from its token on, one in the initial state its column of the outputs.
- * Other columns do not depend on it.
+ * Other columns do not depend on it.  A NaN in log_decay makes its head's outputs
+ * from its token on, and its state, NaN.
  *
  * The workspace holds the end states of the pieces that few long sequences
  * are cut into: ssm_linear_attention_workspace_size() returns its size in bytes

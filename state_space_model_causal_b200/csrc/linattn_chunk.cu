@@ -429,7 +429,8 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                 const double up = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += up;
             }
-            const double before = incl - x[3];
+            // (not incl - x[3]: a NaN would reach the tokens before it)
+            const double up = __shfl_up_sync(0xffffffffu, incl, 1), before = lane ? up : 0.0;
             // the sum at the end of this lane's 32 tokens
             const double end = __shfl_sync(0xffffffffu, incl, lane | 7);
             if (i >= 2) {
@@ -504,7 +505,7 @@ linattn_chunk_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             // (a product of the two factors on the diagonal is exact enough while the first,
             // which is above 1 there, and the second stay well inside float32)
             const float drop = sm.g_hi[s][w * 32] - sm.g_hi[s][w * 32 + 31];
-            bool steep = drop > 100.0f;
+            bool steep = !(drop <= 100.0f);  // (a NaN among the 32: earlier tokens must not meet R)
             if (HT::kScaled) {
                 float mx = 0.0f;
 #pragma unroll 1

@@ -120,3 +120,18 @@ def test_value_channels_far_apart_in_size(io, L):
     want, _ = ref.linear_attention(q, k, v, g)
     bound, _ = bounds(q, k, v, g, None, 1.0, None, io, want, True)
     assert (np.abs(out - want) <= bound + (common_scale(q, k, v, None, 1.0) if io == "f16" else 0.0)).all()
+
+
+@pytest.mark.parametrize("io,L", [("f32", 300), ("bf16", 300), ("f16", 300), ("bf16", 2500), ("f16", 2500)])
+def test_a_decay_that_is_nan_reaches_no_earlier_token(io, L):
+    """Outputs before its token are what they are without it; those from it on, and the
+    state, are NaN.  The other head sees nothing.  L = 2500: a sequence in pieces."""
+    q, k, v, g, s0 = problem(1, 2, 1, L, 64, 64, io, "token", seed=75)
+    at = L - 255  # in the middle of 32 tokens
+    bad = g.copy()
+    bad[0, 1, at] = np.nan
+    skip_out, skip_state = np.zeros(v.shape, bool), np.zeros(s0.shape, bool)
+    skip_out[0, 1, at:] = skip_state[0, 1] = True
+    out, S, kern = run(q, k, v, bad, s0, io=io)
+    assert np.isnan(out[skip_out]).all() and np.isnan(S[skip_state]).all()
+    check((q, k, v, g, s0), (out, S), 1.0, io, kern, skip_out, skip_state)
