@@ -492,8 +492,13 @@ __global__ void __launch_bounds__(kBlock) linattn_step_generic_kernel(const LinA
 
 template <typename ST>
 cudaError_t step_t(const LinAttnStepProblem& p, int grid, cudaStream_t s) {
-    if (p.N / Vec16<ST>::VE <= 32) linattn_step_kernel<ST, 1><<<grid, kBlock, 0, s>>>(p);
-    else linattn_step_kernel<ST, 2><<<grid, kBlock, 0, s>>>(p);
+    if constexpr (Vec16<ST>::VE == 4) {  // (rows of 16-bit numbers are 32 vectors at most)
+        if (p.N > 128) {
+            linattn_step_kernel<ST, 2><<<grid, kBlock, 0, s>>>(p);
+            return cudaGetLastError();
+        }
+    }
+    linattn_step_kernel<ST, 1><<<grid, kBlock, 0, s>>>(p);
     return cudaGetLastError();
 }
 
