@@ -515,8 +515,9 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  *
  *   q, k       (B, Hk, L, N)  f32 | f16 | bf16, one dtype; Hk divides H, 1 <= N <= 256
  *   v, out     (B, H, L, P)   q's dtype
- *   log_decay  (H) or (B, H, L)  f32: the decay's natural logarithm, <= 0 (-inf: forget
- *              all that came before; a positive value counts as 0)
+ *   log_decay  (H) or (B, H, L)  f32: the decay's natural logarithm, <= 0 (-inf: a factor
+ *              of 0, which forgets all that came before and is finite; a positive
+ *              value counts as 0)
  *   state      (B, H, P, N)   f32, optional: S_0 (absent: zeros)
  *   state_out  (B, H, P, N)   f32, optional: the state after the last token.  Absent:
  *              `state`, if given, is updated in place
@@ -561,7 +562,7 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  *   state      (S, H, P, N)   f32 | f16 | bf16: slots of a state cache
  *   q, k       (B, Hk, N)     f32 | f16 | bf16, one dtype
  *   v, out     (B, H, P)      q's dtype
- *   log_decay  (H) or (B, H)  f32
+ *   log_decay  (H) or (B, H)  f32, as above (a positive value counts as 0)
  *   state_batch_indices (B)   i32, optional, as in ssm_selective_state_update: row b
  *              reads and writes slot state_batch_indices[b]; an index outside
  *              [0, S) skips the row.  Without indices S must equal B

@@ -9,13 +9,13 @@ import numpy as np
 
 def linear_attention(q, k, v, log_decay, scale=1.0, state=None, seq_lens=None):
     """q, k (B, Hk, L, N); v (B, H, L, P); log_decay (H) or (B, H, L); state
-    (B, H, P, N).  Token by token: S = exp(g) S + v k^T, out = scale S q.
+    (B, H, P, N).  Token by token: S = exp(min(g, 0)) S + v k^T, out = scale S q.
     Returns (out, S); rows of out at or past seq_lens are NaN."""
     q, k, v = (np.asarray(a, np.float64) for a in (q, k, v))
     B, H, L, P = v.shape
     N, rep = q.shape[3], H // max(q.shape[1], 1)
     q, k = np.repeat(q, rep, axis=1), np.repeat(k, rep, axis=1)
-    g = np.asarray(log_decay, np.float64)
+    g = np.minimum(np.asarray(log_decay, np.float64), 0.0)  # (a NaN stays one)
     g = np.broadcast_to(g[None, :, None] if g.ndim == 1 else g, (B, H, L))
     S = np.zeros((B, H, P, N)) if state is None else np.array(state, np.float64)
     out = np.full((B, H, L, P), np.nan)
@@ -29,12 +29,12 @@ def linear_attention(q, k, v, log_decay, scale=1.0, state=None, seq_lens=None):
 
 def linear_attention_step(state, q, k, v, log_decay, scale=1.0, slots=None):
     """One token: state (S, H, P, N), q, k (B, Hk, N), v (B, H, P), log_decay (H)
-    or (B, H).  Returns (out, new states (B, H, P, N)); rows whose slot is out
+    or (B, H), a positive one counts as 0.  Returns (out, new states (B, H, P, N)); rows whose slot is out
     of range are NaN."""
     state, q, k, v = (np.asarray(a, np.float64) for a in (state, q, k, v))
     B, H = v.shape[:2]
     rep = H // q.shape[1]
-    g = np.broadcast_to(np.asarray(log_decay, np.float64), (B, H))
+    g = np.broadcast_to(np.minimum(np.asarray(log_decay, np.float64), 0.0), (B, H))
     out, new = np.full(v.shape, np.nan), np.full((B,) + state.shape[1:], np.nan)
     for b in range(B):
         s = b if slots is None else int(slots[b])

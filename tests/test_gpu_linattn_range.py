@@ -135,3 +135,14 @@ def test_a_decay_that_is_nan_reaches_no_earlier_token(io, L):
     out, S, kern = run(q, k, v, bad, s0, io=io)
     assert np.isnan(out[skip_out]).all() and np.isnan(S[skip_state]).all()
     check((q, k, v, g, s0), (out, S), 1.0, io, kern, skip_out, skip_state)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("decay", ["head", "token"])
+def test_a_positive_log_decay_counts_as_zero(io, decay):
+    """In a prompt, on both kernels."""
+    q, k, v, g, s0 = problem(2, 4, 2, 150, 64, 64, io, decay, seed=76)
+    up = g.copy()
+    up.reshape(-1)[::3] = np.resize([1e-3, 0.7, 90.0, np.inf], up.reshape(-1)[::3].shape)
+    out, S, kern = run(q, k, v, up, s0, io=io)
+    check((q, k, v, np.minimum(up, 0.0), s0), (out, S), 1.0, io, kern)

@@ -72,3 +72,19 @@ def test_step_layouts(layout, st, io, B, H, Hk, N, P, slots):
         np.testing.assert_array_equal(around, before)
         if not in_place:
             np.testing.assert_array_equal(to_np(S), state)
+
+
+@pytest.mark.parametrize("layout", ["dense", "gaps", "shifted"])
+@pytest.mark.parametrize("per_head", [True, False])
+def test_a_positive_log_decay_counts_as_zero(layout, per_head):
+    from state_space_model_causal_b200 import ssm_linear_attention_update
+    state = gen.round_to(gen.normal((2, 4, 24, 64), "up", "s"), "f32")
+    q, k, v = (draw(s, "f32", "up", x) for s, x in (((2, 2, 64), "q"), ((2, 2, 64), "k"), ((2, 4, 24), "v")))
+    g = np.array([0.5, -0.25, np.inf, 88.0])
+    g = g if per_head else np.stack([g, -g[::-1]])
+    _, S = pool(state, "f32", layout)
+    o = ssm_linear_attention_update(S, T(q, "f32"), T(k, "f32"), T(v, "f32"), T(g, "f32"))
+    g = np.minimum(g, 0.0)
+    out, new = ref.linear_attention_step(state, q, k, v, g)
+    bo, bn = step_bounds(state, q, k, v, g, 1.0, None, "f32", "f32", out, new)
+    assert (np.abs(to_np(o) - out) <= bo).all() and (np.abs(to_np(S) - new) <= bn).all()
