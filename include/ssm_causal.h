@@ -651,7 +651,9 @@ ssm_status ssm_linear_attention_update(const ssm_linattn_update_args* args, void
  *
  * 16-bit types with unit stride along D, D a multiple of 8 up to 128 and 16-byte
  * aligned rows run on SSM_KERNEL_PAGED_DECODE, everything else on
- * SSM_KERNEL_PAGED_DECODE_GENERIC.
+ * SSM_KERNEL_PAGED_DECODE_GENERIC.  The former rounds the weights p to the cache's type
+ * before they meet the values: once where Hq / Hkv > 8 (2^-8 of a weight in bfloat16, 2^-11 in
+ * float16), else twice (2^-16, 2^-22); their sum is of unrounded ones.
  * ------------------------------------------------------------------------ */
 typedef struct ssm_paged_attention_args {
     uint32_t struct_size; /* = sizeof(ssm_paged_attention_args) */
