@@ -428,8 +428,8 @@ def ssm_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_soft
 
     workspace: "auto" (default) passes a cached zero-initialised workspace of
     the size the library asks for (one per device and stream); None passes no
-    workspace (the prefill then runs without hand-overs); a uint8 CUDA tensor
-    is passed as given."""
+    workspace (the prefill then runs without hand-overs); a contiguous CUDA
+    tensor is passed as given."""
     import torch
     if out is None:
         out = torch.empty_like(x)
@@ -453,7 +453,7 @@ def ssm_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_soft
                 ws = _workspace(dev, stream, need.value)
                 a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
         elif workspace is not None:
-            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            a.workspace, a.workspace_bytes = _given_workspace(workspace)
         _check(_run(library().ssm_selective_scan_fwd, a, tensors, stream), "ssm_selective_scan_fwd")
     return out
 
@@ -489,6 +489,14 @@ def _workspace(dev, stream, nbytes):
                 ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
             _workspaces[key] = ws
         return ws
+
+
+def _given_workspace(ws):
+    """Address and size in bytes of a workspace, whose elements have to lie side by
+    side (an expanded tensor has far fewer bytes than elements)."""
+    if not ws.is_contiguous():
+        raise ValueError("a workspace must be a contiguous tensor")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 class _on_device:
@@ -607,8 +615,8 @@ def _empty_like(t, stream):
 def _call_with_workspace(fn, size_fn, what, args, tensors, stream, workspace, optional):
     """Call an entry point whose workspace holds nothing between calls: "auto"
     allocates one for this call on its stream (the caching allocator reuses
-    it; a captured graph gets one of its own), a uint8 CUDA tensor is passed
-    as given, None passes none where the entry point can do without."""
+    it; a captured graph gets one of its own), a contiguous CUDA tensor is
+    passed as given, None passes none where the entry point can do without."""
     import torch
     dev = device_of(tensors if workspace is None or isinstance(workspace, str) else (*tensors, workspace))
     with _on_device(dev):
@@ -626,7 +634,7 @@ def _call_with_workspace(fn, size_fn, what, args, tensors, stream, workspace, op
         elif not optional:
             raise ValueError(f"{what} needs a workspace")
         if ws is not None:
-            args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+            args.workspace, args.workspace_bytes = _given_workspace(ws)
         _check(fn(ctypes.byref(args), handle), what)
 
 
