@@ -648,7 +648,9 @@ def ssm_linear_attention_fwd(q, k, v, log_decay, scale=1.0, state=None, state_ou
     out_t = scale S_t q_t.  q, k (B, Hk, L, N); v (B, H, L, P); log_decay (H)
     or (B, H, L) float32, a positive value counts as 0; state (B, H, P, N)
     float32, read as S_0 and updated in place, or only read when state_out is
-    given; seq_lens (B) int32.  Without ``out``, the output takes v's order of dimensions.  Returns out."""
+    given; seq_lens (B) int32.  Without ``out`` the output takes v's order of
+    dimensions, and rows at or past seq_lens, which are never written, hold
+    anything.  Returns out."""
     if out is None:
         out = _empty_like(v, stream)
     tensors = (q, k, v, log_decay, state, state_out, seq_lens, out)
@@ -669,7 +671,9 @@ def ssm_linear_attention_update(state, q, k, v, log_decay, scale=1.0, state_batc
     """One token of linear attention per sequence (see include/ssm_causal.h).
     state (S, H, P, N); q, k (B, Hk, N); v (B, H, P); log_decay (H) or (B, H)
     float32, a positive value counts as 0; state_batch_indices (B) int32 slots.
-    The state is updated in place, or written to state_out and only read.  Returns out (B, H, P)."""
+    The state is updated in place, or written to state_out and only read.
+    Without ``out``, rows whose slot is outside the cache, which are never
+    written, hold anything.  Returns out (B, H, P)."""
     if out is None:
         out = _empty_like(v, stream)
     tensors = (state, q, k, v, log_decay, state_batch_indices, state_out, out)
