@@ -544,11 +544,14 @@ ssm_status ssm_selective_state_update(const ssm_ssu_args* args, void* stream);
  * is held in float32; what a token adds to it enters as a sum of 16-bit
  * numbers (two for float16, three for bfloat16), which loses at most 2^-22 of
  * it -- in float16, where 64 value channels of a chunk share a power of two,
- * 2^-49 of their largest if that is more.  An infinity counts as a NaN there:
+ * 2^-49 of their largest if that is more.  The tensor cores align products by
+ * the exponents of their factors: a float16 subnormal among q, k, v is as
+ * accurate there as a number of 2^-14.  An infinity counts as a NaN there:
  * one in v makes its column of the outputs from its token on, and of the state, NaN,
  * one in k every output from its token on, one in the initial state its column of the outputs.
  * Other columns do not depend on it.  A NaN in log_decay makes its head's outputs
- * from its token on, and its state, NaN.
+ * from its token on, and its state, NaN.  On the generic kernel an infinity in v
+ * or the state may become a NaN at the next token.
  *
  * The workspace holds the end states of the pieces that few long sequences
  * are cut into: ssm_linear_attention_workspace_size() returns its size in bytes
