@@ -428,8 +428,8 @@ def ssm_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_soft
 
     workspace: "auto" (default) passes a cached zero-initialised workspace of
     the size the library asks for (one per device and stream); None passes no
-    workspace (the prefill then runs without hand-overs); a contiguous CUDA
-    tensor is passed as given."""
+    workspace (the prefill then runs without hand-overs); a uint8 CUDA tensor
+    is passed as given."""
     import torch
     if out is None:
         out = torch.empty_like(x)
@@ -492,11 +492,12 @@ def _workspace(dev, stream, nbytes):
 
 
 def _given_workspace(ws):
-    """Address and size in bytes of a workspace, whose elements have to lie side by
-    side (an expanded tensor has far fewer bytes than elements)."""
-    if not ws.is_contiguous():
-        raise ValueError("a workspace must be a contiguous tensor")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    """Address and size in bytes of a workspace: its elements, or the memory from the
+    first to the last of them if that is less (an expanded tensor)."""
+    n = ws.numel()
+    if n > 0 and not ws.is_contiguous():
+        n = min(n, 1 + sum((size - 1) * stride for size, stride in zip(ws.shape, ws.stride())))
+    return ws.data_ptr(), n * ws.element_size()
 
 
 class _on_device:
@@ -615,8 +616,8 @@ def _empty_like(t, stream):
 def _call_with_workspace(fn, size_fn, what, args, tensors, stream, workspace, optional):
     """Call an entry point whose workspace holds nothing between calls: "auto"
     allocates one for this call on its stream (the caching allocator reuses
-    it; a captured graph gets one of its own), a contiguous CUDA tensor is
-    passed as given, None passes none where the entry point can do without."""
+    it; a captured graph gets one of its own), a uint8 CUDA tensor is passed
+    as given, None passes none where the entry point can do without."""
     import torch
     dev = device_of(tensors if workspace is None or isinstance(workspace, str) else (*tensors, workspace))
     with _on_device(dev):
